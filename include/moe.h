@@ -288,6 +288,108 @@ int moe_layer_forward_noalloc(const void *x, int32_t x_dtype, const float *logit
                               float *y, int32_t *topk_idx_out, float *topk_w_out, int32_t *heat,
                               int32_t path, int64_t stream);
 
+/*
+ * Dense operators: the 16-bit parts of the same model next to the routed
+ * layer (a shared expert kept in bf16, dense feed-forward layers, the
+ * projections around them), forward and backward.
+ *
+ * Weights are bf16, row by row: [out][in], the router matrix's order.
+ * Activations are fp32 or bf16.  Products are exact (an fp32 activation
+ * enters as three bf16 terms that sum to it exactly), sums are fp32; results
+ * are rounded once to their type.  The same inputs give the same bits on
+ * every run, whatever else runs.  Row t of every row-wise result depends on
+ * row t of the inputs alone; rows of a buffer past T are neither read nor
+ * written.  Infinities and NaN in a row stay in it.
+ *
+ * Widths (in, out, hidden, ffn) are multiples of 8, at most 2^20; any T from
+ * 0 to 2^24.  T = 0 writes nothing, except that weight gradients (sums over
+ * no rows) are set to zero, or left as they are when accumulating.
+ *
+ * The conventions above hold: contiguous tensors, 16-byte aligned pointers
+ * (checked: MOE_ERR_INVALID_ARG), a workspace of the caller, zero-filled
+ * before its first use and not shared by calls that run at the same time.
+ * One workspace, large enough for each, serves these calls and the routed
+ * layer's in turn; sized for T rows it also serves fewer.  Outputs may not
+ * overlap inputs, except that y may be the residual itself (same type).
+ */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SILU 1       /* v / (1 + exp(-v)) */
+#define MOE_ACT_GELU 2       /* v (1 + erf(v / sqrt 2)) / 2 */
+#define MOE_ACT_GELU_TANH 3  /* v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2 */
+#define MOE_ACT_RELU 4       /* max(v, 0) */
+
+/* Weights of a dense gated feed-forward block (host struct; device pointers
+ * to bf16 matrices). */
+typedef struct moe_dense_ffn {
+    const void *gate, *up;  /* (device) [ffn][hidden] */
+    const void *down;       /* (device) [hidden][ffn] */
+    int32_t hidden, ffn;
+    int32_t act;            /* MOE_ACT_*, applied to the gate projection */
+} moe_dense_ffn;
+
+/* Workspace bytes (device) for moe_linear and moe_linear_backward with up to
+ * T rows of any type; a negative MOE_ERR_* for invalid sizes.  Pure host
+ * function. */
+int64_t moe_linear_workspace_bytes(int32_t T, int32_t in, int32_t out);
+
+/*
+ * Matrix product with bias, activation and residual:
+ *     z = x w^T + bias,   y = act(z) + residual
+ * x (device) [T][in] fp32 or bf16; w (device) bf16 [out][in]; bias (device,
+ * may be NULL) bf16 [out]; residual (device, may be NULL) [T][out] in
+ * r_dtype; y (device) [T][out] in y_dtype.  z (device, may be NULL) bf16
+ * [T][out] receives the pre-activation that moe_linear_backward reads.
+ */
+int moe_linear(const void *x, int32_t x_dtype, int32_t T, int32_t in, const void *w, int32_t out, const void *bias,
+               int32_t act, const void *residual, int32_t r_dtype, void *z, void *y, int32_t y_dtype, void *ws,
+               int64_t ws_bytes, int64_t stream);
+
+/*
+ * Its backward pass (dy, x, w and z bf16):
+ *     dz = dy act'(z),   dx = dz w,   dw = dz^T x,   dbias = sum_t dz_t
+ * (the residual's gradient is dy).  dx (device) bf16 [T][in]; dw (device)
+ * [out][in] and dbias (device) [out] in dw_dtype; each may be NULL, at least
+ * one is not.  accumulate != 0: dw and dbias are added to what they hold.
+ * z is read unless act is MOE_ACT_NONE.  With an activation, dz enters the
+ * products rounded to bf16 (dbias sums the unrounded values).  The
+ * derivative of MOE_ACT_RELU at 0 is 0.
+ */
+int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, const void *x, const void *w, const void *z,
+                        int32_t act, void *dx, void *dw, void *dbias, int32_t dw_dtype, int32_t accumulate, void *ws,
+                        int64_t ws_bytes, int64_t stream);
+
+/* Workspace bytes (device) for moe_gated_ffn and moe_gated_ffn_backward with
+ * up to T rows of any type; a negative MOE_ERR_* for invalid sizes.  Pure
+ * host function. */
+int64_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t hidden, int32_t ffn);
+
+/*
+ * Gated feed-forward block (the formula of an expert, step 3 above):
+ *     g = x gate^T,  u = x up^T,  h = act(g) u,  y = h down^T + residual
+ * x (device) [T][hidden] fp32 or bf16; residual (device, may be NULL)
+ * [T][hidden] in r_dtype; y (device) [T][hidden] in y_dtype.  With residual
+ * = y = moe_layer_forward's fp32 output (shared = NULL there) the block is
+ * that layer's shared expert in bf16.  gu (device, may be NULL) bf16
+ * [T][2*ffn] receives g (columns 0..ffn-1) and u for the backward pass.
+ * h enters the down product rounded to bf16 when y is bf16, exactly (three
+ * bf16 terms) when y is fp32.
+ */
+int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn *w, const void *residual, int32_t r_dtype,
+                  void *gu, void *y, int32_t y_dtype, void *ws, int64_t ws_bytes, int64_t stream);
+
+/*
+ * Its backward pass (dy and x bf16 [T][hidden], gu as moe_gated_ffn wrote it):
+ *     dh = dy down,  dg = dh u act'(g),  du = dh act(g)
+ *     dx = dg gate + du up,  dgate = dg^T x,  dup = du^T x,  ddown = dy^T h
+ * dx (device) bf16 [T][hidden]; dgate, dup (device) [ffn][hidden] and ddown
+ * (device) [hidden][ffn] in dw_dtype; each may be NULL, at least one is not.
+ * accumulate != 0: the weight gradients are added to what they hold.  h, dg
+ * and du enter their products rounded to bf16.
+ */
+int moe_gated_ffn_backward(const void *dy, const void *x, int32_t T, const moe_dense_ffn *w, const void *gu, void *dx,
+                           void *dgate, void *dup, void *ddown, int32_t dw_dtype, int32_t accumulate, void *ws,
+                           int64_t ws_bytes, int64_t stream);
+
 #ifdef __cplusplus
 }
 #endif

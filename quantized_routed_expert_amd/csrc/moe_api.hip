@@ -82,9 +82,6 @@ struct Layout {
 // layout, so a workspace that is zero before its first use stays valid for
 // calls of any shape and path (each call returns the counters to zero).  Each
 // counter has a 256-byte line of its own.
-// after the slot and slice counters: the error word (a line of its own),
-// then the per-workgroup epochs
-constexpr size_t COUNTER_WORDS = (size_t)(2 * DEC_MAX_SLOTS + DEC_MAX_SLICES + 1) * DEC_CSTRIDE + EPOCH_SLOTS;
 // byte offset of the error word (and, after it, the tag of the last call whose wait ran out)
 constexpr size_t ERR_OFFSET = (size_t)(2 * DEC_MAX_SLOTS + DEC_MAX_SLICES) * DEC_CSTRIDE * 4;
 Layout make_layout(int T, int E, int k, int H, int F, int Fs, int path) {
@@ -396,6 +393,15 @@ bool split_fits(int T, int E, int k, int H, int F, int Fs, int bits, int dbits, 
 }
 
 }  // namespace
+
+namespace moe {
+int device_cus(int &cus) {
+    DevInfo dv;
+    const int rc = dev_info(dv);
+    cus = dv.cus;
+    return rc;
+}
+}  // namespace moe
 
 extern "C" {
 

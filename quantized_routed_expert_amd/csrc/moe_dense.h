@@ -1,0 +1,566 @@
+// moe_dense.h -- the tiled bf16 product under the dense operators (linear and
+// the gated feed-forward block, forward and backward).
+//
+// One workgroup computes a BM x BN tile of C over a range of 64-k steps.  Both
+// operands' slices of a step stream into LDS with 16-byte direct-to-LDS buffer
+// loads, double buffered: the loads of step s+1 are in flight while step s is
+// multiplied.  Loads past an operand's edge return zero (the buffer's range
+// check by rows, a per-lane mask along the contiguous axis), so every size
+// that is a multiple of 8 along the contiguous axes runs the same code and no
+// out-of-range value (a NaN next to the matrix) enters a sum.
+//
+// The weight side (N) feeds the MFMA's row operand, the activation side (M)
+// its column operand: D's rows are n, four consecutive per lane, so a lane
+// holds runs along the output's contiguous axis.
+//
+// An operand whose rows run along k is read as 16-byte fragments (8 k); one
+// whose rows run along m or n ("transposed") with ds_read_b64_tr_b16, which
+// hands 16 lanes the columns of a 4 x 16 block.  Both give a lane of k-group
+// g the k values 8g .. 8g+7 in order.
+//
+// LDS placement.  k-rows: 128 bytes (8 pieces of 16) per row, piece c of row r
+// at c ^ s(r); the eight rows a quarter wave reads together have eight
+// different s, so they touch all banks once.  Transposed: R*2 bytes per k,
+// the 32-byte column block p of row k at p ^ g(k) within each 256 bytes; the
+// eight k rows half a wave reads together have eight different g.  Direct
+// loads write LDS in lane order, so the permutation is applied to the global
+// address (within 128 or 256 contiguous bytes: the same cache lines).
+#pragma once
+#include "moe_device.h"
+
+namespace moe {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+
+constexpr uint32_t DN_OOB = 0x80000000u;  // past every buffer's range (< 2^31 bytes)
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t dn_rsrc(const void *p, int64_t bytes) {
+    const int n = bytes <= 0 ? 0 : (bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, n, 0x00027000);
+}
+
+// ---------------------------------------------------------------------------
+// Values and types
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float dn_bf(uint32_t bits16) { return __builtin_bit_cast(float, bits16 << 16); }
+// two floats -> two bf16, round to nearest even (NaN kept)
+__device__ __forceinline__ uint32_t dn_pack(float a, float b) {
+    const __bf16 x = (__bf16)a, y = (__bf16)b;
+    return (uint32_t)__builtin_bit_cast(uint16_t, x) | ((uint32_t)__builtin_bit_cast(uint16_t, y) << 16);
+}
+
+// V consecutive bf16 / fp32 (16-byte aligned when V is 8, 8-byte for bf16 V = 4)
+template <int V>
+__device__ __forceinline__ void dn_load_bf(const uint16_t *p, float (&v)[V]) {
+    if constexpr (V == 8) {
+        const u32x4 q = *(const u32x4 *)p;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = dn_bf(w[i] & 0xFFFFu);
+            v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+        }
+    } else {
+        const u32x2 q = *(const u32x2 *)p;
+        v[0] = dn_bf(q.x & 0xFFFFu);
+        v[1] = __builtin_bit_cast(float, q.x & 0xFFFF0000u);
+        v[2] = dn_bf(q.y & 0xFFFFu);
+        v[3] = __builtin_bit_cast(float, q.y & 0xFFFF0000u);
+    }
+}
+template <int V>
+__device__ __forceinline__ void dn_load_f32(const float *p, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4v q = *(const float4v *)(p + i);
+        v[i] = q.x;
+        v[i + 1] = q.y;
+        v[i + 2] = q.z;
+        v[i + 3] = q.w;
+    }
+}
+template <int V>
+__device__ __forceinline__ void dn_store_bf(uint16_t *p, const float (&v)[V]) {
+    if constexpr (V == 8)
+        *(u32x4 *)p = u32x4{dn_pack(v[0], v[1]), dn_pack(v[2], v[3]), dn_pack(v[4], v[5]), dn_pack(v[6], v[7])};
+    else
+        *(u32x2 *)p = u32x2{dn_pack(v[0], v[1]), dn_pack(v[2], v[3])};
+}
+template <int V>
+__device__ __forceinline__ void dn_store_f32(float *p, const float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *(float4v *)(p + i) = float4v{v[i], v[i + 1], v[i + 2], v[i + 3]};
+}
+
+// An fp32 value as three bf16 terms: 8 significant bits each, cut toward
+// zero, so the terms sum to the value exactly (24 bits) unless the last ones
+// underflow.  Infinities and NaN stay in the first term alone.
+__device__ __forceinline__ void dn_split3(float v, uint32_t (&t)[3]) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    if ((u & 0x7F800000u) == 0x7F800000u) {
+        t[0] = (u >> 16) | ((u & 0x007FFFFFu) ? 0x40u : 0u);  // (a NaN keeps a mantissa bit)
+        t[1] = t[2] = 0u;
+        return;
+    }
+    t[0] = u >> 16;
+    const float r1 = v - __builtin_bit_cast(float, u & 0xFFFF0000u);  // exact
+    const uint32_t u1 = __builtin_bit_cast(uint32_t, r1);
+    t[1] = u1 >> 16;
+    const float r2 = r1 - __builtin_bit_cast(float, u1 & 0xFFFF0000u);  // exact, at most 8 bits
+    t[2] = __builtin_bit_cast(uint32_t, r2) >> 16;
+}
+template <int V>
+__device__ __forceinline__ void dn_store_split3(uint16_t *p, size_t plane, const float (&v)[V]) {
+    uint32_t t[V][3];
+#pragma unroll
+    for (int i = 0; i < V; ++i) dn_split3(v[i], t[i]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *(u32x2 *)(p + k * plane + i) = u32x2{t[i][k] | (t[i + 1][k] << 16), t[i + 2][k] | (t[i + 3][k] << 16)};
+}
+
+// ---------------------------------------------------------------------------
+// Activations in fp32.  The logistic function 1 / (1 + exp(-v)): exp
+// overflows to infinity for large -v, which gives 0, its limit.
+// GELU (tanh) uses (1 + tanh(q)) / 2 = logistic(2 q).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float dn_sigmoid(float v) { return __builtin_amdgcn_rcpf(1.0f + __expf(-v)); }
+constexpr float DN_GELU_C = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float DN_GELU_A = 0.044715f;
+
+// act(v); with D, its derivative too
+template <bool D>
+__device__ __forceinline__ float dn_act1(int act, float v, float &d) {
+    switch (act) {
+        case DN_ACT_SILU: {
+            const float s = dn_sigmoid(v);
+            if (D) d = s * (1.0f + v * (1.0f - s));
+            return v * s;
+        }
+        case DN_ACT_GELU: {
+            const float c = 0.5f * (1.0f + erff(v * 0.70710678118654752f));
+            if (D) d = c + v * 0.3989422804014327f * __expf(-0.5f * v * v);
+            return v * c;
+        }
+        case DN_ACT_GELU_TANH: {
+            const float s = dn_sigmoid(2.0f * DN_GELU_C * (v + DN_GELU_A * v * v * v));
+            if (D) d = s + 2.0f * v * s * (1.0f - s) * DN_GELU_C * (1.0f + 3.0f * DN_GELU_A * v * v);
+            return v * s;
+        }
+        case DN_ACT_RELU:
+            if (D) d = v > 0.0f ? 1.0f : 0.0f;
+            return v > 0.0f ? v : (v != v ? v : 0.0f);
+        default:
+            if (D) d = 1.0f;
+            return v;
+    }
+}
+template <int V>
+__device__ __forceinline__ void dn_act(int act, float (&v)[V]) {
+    float d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = dn_act1<false>(act, v[i], d);
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues: V consecutive columns from n on of row m
+// ---------------------------------------------------------------------------
+// z = v + bias (kept in bf16 if asked); y = act(z) + residual
+template <int V>
+__device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
+    const int64_t at = m * N + n;
+    if (e.bias) {
+        float b[V];
+        dn_load_bf<V>(e.bias + n, b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += b[i];
+    }
+    if (e.z) dn_store_bf<V>(e.z + at, v);
+    if (e.act) dn_act<V>(e.act, v);
+    if (e.res) {
+        float r[V];
+        if (e.res_f32)
+            dn_load_f32<V>((const float *)e.res + at, r);
+        else
+            dn_load_bf<V>((const uint16_t *)e.res + at, r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += r[i];
+    }
+    if (e.y_f32)
+        dn_store_f32<V>((float *)e.y + at, v);
+    else
+        dn_store_bf<V>((uint16_t *)e.y + at, v);
+}
+// h = act(g) u.  h enters the down product in bf16; with h_terms = 3 (an fp32
+// y) as three exact bf16 terms, so that y is as good as its type.  g and u
+// kept for the backward pass are rounded to bf16 (the type that pass reads).
+template <int V>
+__device__ __forceinline__ void dn_epi_gated(const DenseEpi &e, int64_t M, int N, int64_t m, int n, float (&g)[V],
+                                             float (&u)[V]) {
+    if (e.gu) {
+        dn_store_bf<V>(e.gu + m * (2 * (int64_t)N) + n, g);
+        dn_store_bf<V>(e.gu + m * (2 * (int64_t)N) + N + n, u);
+    }
+    dn_act<V>(e.act, g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] *= u[i];
+    if (e.h_terms == 3)
+        dn_store_split3<V>(e.h + m * N + n, (size_t)M * N, g);
+    else
+        dn_store_bf<V>(e.h + m * N + n, g);
+}
+// v = dh: h = act(g) u, dg = dh u act'(g), du = dh act(g), each rounded once
+// to bf16, the type their products take
+template <int V>
+__device__ __forceinline__ void dn_epi_dgated(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
+    float g[V], u[V], h[V], dg[V], du[V];
+    const int64_t at = m * (2 * (int64_t)N) + n;
+    dn_load_bf<V>(e.gu_in + at, g);
+    dn_load_bf<V>(e.gu_in + at + N, u);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float d;
+        const float a = dn_act1<true>(e.act, g[i], d);
+        h[i] = a * u[i];
+        dg[i] = v[i] * u[i] * d;
+        du[i] = v[i] * a;
+    }
+    if (e.h) dn_store_bf<V>(e.h + m * N + n, h);
+    dn_store_bf<V>(e.dgu + at, dg);
+    dn_store_bf<V>(e.dgu + at + N, du);
+}
+// weight gradient: row m of y, or of y2 from m_split on
+template <int V>
+__device__ __forceinline__ void dn_epi_grad(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
+    void *y = e.y;
+    if (m >= e.m_split) {
+        y = e.y2;
+        m -= e.m_split;
+    }
+    if (!y) return;
+    const int64_t at = m * N + n;
+    if (e.accumulate) {  // on what is there, in its own type
+        float r[V];
+        if (e.y_f32)
+            dn_load_f32<V>((const float *)y + at, r);
+        else
+            dn_load_bf<V>((const uint16_t *)y + at, r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += r[i];
+    }
+    if (e.y_f32)
+        dn_store_f32<V>((float *)y + at, v);
+    else
+        dn_store_bf<V>((uint16_t *)y + at, v);
+}
+template <int EPI, int V>
+__device__ __forceinline__ void dn_epi(const DenseParams &P, int64_t m, int n, float (&v)[V]) {
+    if constexpr (EPI == DN_EPI_LINEAR) dn_epi_linear<V>(P.e, P.N, m, n, v);
+    if constexpr (EPI == DN_EPI_DGATED) dn_epi_dgated<V>(P.e, P.N, m, n, v);
+    if constexpr (EPI == DN_EPI_GRAD) dn_epi_grad<V>(P.e, P.N, m, n, v);
+}
+
+// ---------------------------------------------------------------------------
+// Streaming one operand's slices into LDS
+// ---------------------------------------------------------------------------
+// KC: R rows of 64 k.  SH: the bit of the row that joins its two low bits in
+// s(r) (2: fragments of 16 consecutive rows; 3, 4: rows in runs of 2 or 4
+// fragments, see dn_row).  Otherwise: 64 k of R columns.
+template <int R, bool KC, int NW, int SH>
+struct DnStream {
+    static constexpr int NL = R * 128 / 1024 / NW;  // loads per wave and step
+    static constexpr int BYTES = R * 128;
+    static_assert(R * 128 % (1024 * NW) == 0, "whole wave loads");
+    uint32_t voff[NL];
+
+    // ld in elements; cols: columns left from the tile's first (transposed)
+    __device__ __forceinline__ void setup(int wave, int lane, int64_t ld, int64_t cols) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            if constexpr (KC) {
+                const int r = (j * NW + wave) * 8 + (lane >> 3);
+                voff[j] = (uint32_t)(r * (int)ld * 2 + piece(j, wave, lane) * 16);
+            } else {
+                const int at = (j * NW + wave) * 1024 + lane * 16;
+                const int k = at / (R * 2), p = (at % (R * 2)) / 16;
+                const int g = (k & 3) | (((k >> 3) & 1) << 2);
+                const int c = p ^ (g << 1);
+                voff[j] = c * 8 < cols ? (uint32_t)(k * (int)ld * 2 + c * 16) : DN_OOB;
+            }
+        }
+    }
+    // the 16-byte piece of its row that lane loads (k-rows)
+    __device__ __forceinline__ static int piece(int j, int wave, int lane) {
+        const int r = (j * NW + wave) * 8 + (lane >> 3);
+        return (lane & 7) ^ ((r & 3) | (((r >> SH) & 1) << 2));
+    }
+    // k-rows: base = the tile's first row at k0, kleft = K - k0 (> 0); rows
+    // left is in the buffer's size.  b2: second half of every 64 rows (gated)
+    __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t r, lds_u8 *dst, int wave, int lane, int kleft) {
+        if (KC && kleft < DN_BK) {
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const uint32_t v = piece(j, wave, lane) * 8 < kleft ? voff[j] : DN_OOB;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst + (j * NW + wave) * 1024, 16, v, 0, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NL; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst + (j * NW + wave) * 1024, 16, voff[j], 0, 0, 0);
+        }
+    }
+};
+
+// Row of the tile that row i of fragment j stands for: CG fragments share a
+// run of 16 CG rows, four consecutive ones each in turn, so that a lane's CG
+// results are 4 CG consecutive rows.
+template <int CG>
+__device__ __forceinline__ constexpr int dn_row(int i, int j) {
+    return (i >> 2) * 4 * CG + (j % CG) * 4 + (i & 3) + (j / CG) * 16 * CG;
+}
+
+// Workgroup -> tile: workgroups go round robin over the 8 XCDs, so each XCD
+// gets a contiguous run of the tile order; the order walks groups of 8 tile
+// rows column by column, so the tiles an XCD works on at a time share rows of
+// both operands in its L2.
+__device__ __forceinline__ void dn_tile(const DenseParams &P, int b, int &tm, int &tn) {
+    const int total = P.tiles_m * P.tiles_n;
+    const int q = total >> 3, r = total & 7, x = b & 7;
+    const int t = x * q + min(x, r) + (b >> 3);
+    constexpr int G = 8;
+    const int per = G * P.tiles_n;
+    const int grp = t / per, in = t - grp * per;
+    const int rows = min(G, P.tiles_m - grp * G);
+    tn = in / rows;
+    tm = grp * G + in - tn * rows;
+}
+
+template <int BM, int BN, int WM, int WN, int FORM, int EPI>
+__global__ __launch_bounds__(WM *WN * 64, 2) void k_dense(DenseParams P) {
+#ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the stub alone: it drops stubs of templates that use the buffer builtins)
+    constexpr int NW = WM * WN;
+    constexpr bool AKC = FORM != DN_TN, BKC = FORM == DN_NT;
+    constexpr bool GATED = EPI == DN_EPI_GATED;
+    constexpr int MS = BM / WM / 16, NS = BN / WN / 16;  // 16 x 16 blocks per wave
+    constexpr int CG = BKC ? (GATED ? 2 : 4) : 1;        // (transposed reads keep 16 consecutive columns)
+    constexpr int SHB = CG == 4 ? 4 : CG == 2 ? 3 : 2;
+    static_assert(!GATED || NS == 4, "gate and up halves of 64 weight rows");
+    static_assert(NS % CG == 0, "whole runs");
+    typedef DnStream<BM, AKC, NW, 2> SA;
+    typedef DnStream<BN, BKC, NW, SHB> SB;
+    constexpr int STAGE = SA::BYTES + SB::BYTES;
+    __shared__ __align__(1024) uint8_t smem[2 * STAGE];
+    lds_u8 *const lds = (lds_u8 *)smem;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    int tm, tn;
+    dn_tile(P, blockIdx.x, tm, tn);
+    const int64_t m0 = (int64_t)tm * BM;
+    constexpr int BNF = GATED ? BN / 2 : BN;  // output columns per tile
+    const int64_t n0 = (int64_t)tn * BNF;
+    const int s_end = min(P.steps, ((int)blockIdx.y + 1) * P.steps_per_split);
+    int s = (int)blockIdx.y * P.steps_per_split;
+
+    SA sa;
+    SB sb;
+    // the product (of the sum) and k that the next loads take
+    int seg = 0, k0 = s * DN_BK;
+    while (seg + 1 < P.nseg && k0 >= (P.seg[seg].K + DN_BK - 1) / DN_BK * DN_BK) {
+        k0 -= (P.seg[seg].K + DN_BK - 1) / DN_BK * DN_BK;
+        ++seg;
+    }
+    sa.setup(wave, lane, P.seg[0].lda, P.M - m0);
+    // gated: the tile's 64-row groups hold 32 gate rows, then the same 32 up rows
+    if constexpr (GATED) {
+        static_assert(!GATED || SB::NL * NW * 8 == BN, "rows per load");
+#pragma unroll
+        for (int j = 0; j < SB::NL; ++j) {
+            const int r = (j * NW + wave) * 8 + (lane >> 3);
+            const int f = (r >> 6) * 32 + (r & 31);
+            sb.voff[j] = (uint32_t)(f * (int)P.seg[0].ldb * 2 + SB::piece(j, wave, lane) * 16);
+        }
+    } else {
+        sb.setup(wave, lane, P.seg[0].ldb, P.N - n0);
+    }
+
+    auto load = [&](int buf) {
+        const DenseSeg &g = P.seg[seg];
+        lds_u8 *da = lds + buf * STAGE, *db = da + SA::BYTES;
+        const int kleft = g.K - k0;
+        if constexpr (AKC)
+            sa.issue(dn_rsrc(g.a + m0 * g.lda + k0, ((int64_t)min((int64_t)BM, P.M - m0) * g.lda - k0) * 2), da, wave, lane,
+                     kleft);
+        else
+            sa.issue(dn_rsrc(g.a + k0 * g.lda + m0, ((int64_t)min(DN_BK, kleft) * g.lda - m0) * 2), da, wave, lane, kleft);
+        if constexpr (GATED) {
+            const int64_t bytes = ((int64_t)min((int64_t)BNF, P.N - n0) * g.ldb - k0) * 2;
+            const __amdgpu_buffer_rsrc_t rg = dn_rsrc(g.b + n0 * g.ldb + k0, bytes), ru = dn_rsrc(g.b2 + n0 * g.ldb + k0, bytes);
+#pragma unroll
+            for (int j = 0; j < SB::NL; ++j) {
+                uint32_t v = sb.voff[j];
+                if (kleft < DN_BK) v = SB::piece(j, wave, lane) * 8 < kleft ? v : DN_OOB;
+                const bool up = (((j * NW + wave) * 8) >> 5) & 1;
+                if (up)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, db + (j * NW + wave) * 1024, 16, v, 0, 0, 0);
+                else
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rg, db + (j * NW + wave) * 1024, 16, v, 0, 0, 0);
+            }
+        } else if constexpr (BKC) {
+            sb.issue(dn_rsrc(g.b + n0 * g.ldb + k0, ((int64_t)min((int64_t)BN, P.N - n0) * g.ldb - k0) * 2), db, wave, lane,
+                     kleft);
+        } else {
+            sb.issue(dn_rsrc(g.b + k0 * g.ldb + n0, ((int64_t)min(DN_BK, kleft) * g.ldb - n0) * 2), db, wave, lane, kleft);
+        }
+        k0 += DN_BK;
+        if (k0 >= g.K) {
+            k0 = 0;
+            ++seg;
+        }
+    };
+
+    float4v acc[MS][NS];
+#pragma unroll
+    for (int i = 0; i < MS; ++i)
+#pragma unroll
+        for (int j = 0; j < NS; ++j) acc[i][j] = float4v{0.f, 0.f, 0.f, 0.f};
+
+    // fragment addresses within a stage
+    const int li = lane & 15, lg = lane >> 4;
+    const int a_row = wm * (BM / WM), b_row = wn * (BN / WN);
+    const uint32_t a_kc = (uint32_t)((a_row + li) * 128 + ((lg ^ (li & 7)) << 4));
+    const uint32_t b_kc = (uint32_t)((b_row + dn_row<CG>(li, 0)) * 128 + ((lg ^ (li & 7)) << 4));
+    const int tg = (li >> 2) | ((lg & 1) << 2);  // g(k) of the k rows this lane addresses
+    const int tk = 8 * lg + (li >> 2);
+    const uint32_t a_tr = (uint32_t)(tk * BM * 2 + (li & 3) * 8), b_tr = (uint32_t)(tk * BN * 2 + (li & 3) * 8);
+
+    auto frag_kc = [&](lds_u8 *base, uint32_t at, int row, int kk) {
+        return *(lds_bf16x8 *)(base + ((at ^ (kk << 6)) + row * 128));
+    };
+    auto frag_tr = [&](lds_u8 *base, uint32_t at, int blk, int ld2, int kk) {
+        const uint32_t o = at + (((blk ^ tg)) << 5) + kk * 32 * ld2;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(base + o));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(base + o + 4 * ld2));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(bf16x8, s16x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
+    };
+
+    if (s < s_end) load(0);
+    for (int buf = 0; s < s_end; ++s, buf ^= 1) {
+        wait_vm<0>();   // this wave's loads of step s have landed
+        lds_barrier();  // every wave's have, and every wave has read step s-1
+        if (s + 1 < s_end) load(buf ^ 1);
+        lds_u8 *ba = lds + buf * STAGE, *bb = ba + SA::BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            bf16x8 fb[NS], fa[MS];
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                fb[j] = BKC ? frag_kc(bb, b_kc, dn_row<CG>(0, j), kk) : frag_tr(bb, b_tr, b_row / 16 + j, BN * 2, kk);
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+                fa[i] = AKC ? frag_kc(ba, a_kc, 16 * i, kk) : frag_tr(ba, a_tr, a_row / 16 + i, BM * 2, kk);
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        }
+    }
+
+    // results: row m = 16 i + li, columns from 4 CG lg on
+    constexpr int V = CG == 1 ? 4 : 8;
+#pragma unroll
+    for (int i = 0; i < MS; ++i) {
+        const int64_t m = m0 + a_row + 16 * i + li;
+        if (m >= P.M) continue;
+        if constexpr (GATED) {
+            const int n = (int)n0 + wn * 32 + 8 * lg;
+            if (n >= P.N) continue;
+            float g[8], u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                g[k] = acc[i][k >> 2][k & 3];
+                u[k] = acc[i][2 + (k >> 2)][k & 3];
+            }
+            if (P.splits > 1) {
+                float *p = P.part + ((int64_t)blockIdx.y * P.M + m) * (2 * (int64_t)P.N) + n;
+                dn_store_f32<8>(p, g);
+                dn_store_f32<8>(p + P.N, u);
+            } else {
+                dn_epi_gated<8>(P.e, P.M, P.N, m, n, g, u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NS * 4 / V; ++j) {
+                const int jj = j * (V / 4);
+                const int n = (int)n0 + b_row + dn_row<CG>(4 * lg, jj);
+                if (n >= P.N) continue;
+                float v[V];
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[k] = acc[i][jj + (k >> 2)][k & 3];
+                if (P.splits > 1)
+                    dn_store_f32<V>(P.part + ((int64_t)blockIdx.y * P.M + m) * P.N + n, v);
+                else
+                    dn_epi<EPI, V>(P, m, n, v);
+            }
+        }
+    }
+#endif
+}
+
+// The sum of a split product's parts, in their order, and the epilogue.
+template <int EPI>
+__global__ __launch_bounds__(256) void k_dense_join(DenseParams P) {
+    const int64_t per = P.N / 8, total = per * P.M;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
+        const int64_t m = q / per;
+        const int n = (int)(q - m * per) * 8;
+        constexpr bool GATED = EPI == DN_EPI_GATED;
+        const int64_t ld = GATED ? 2 * (int64_t)P.N : P.N;
+        const float *p = P.part + m * ld + n;
+        float v[8], u[8];
+        dn_load_f32<8>(p, v);
+        if constexpr (GATED) dn_load_f32<8>(p + P.N, u);
+        for (int s = 1; s < P.splits; ++s) {
+            float w[8];
+            p += (int64_t)P.M * ld;
+            dn_load_f32<8>(p, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += w[i];
+            if constexpr (GATED) {
+                dn_load_f32<8>(p + P.N, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] += w[i];
+            }
+        }
+        if constexpr (GATED)
+            dn_epi_gated<8>(P.e, P.M, P.N, m, n, v, u);
+        else
+            dn_epi<EPI, 8>(P, m, n, v);
+    }
+}
+
+// One product of the given form and epilogue, and its join when it is split.
+template <int FORM, int EPI>
+hipError_t dense_launch_t(const DenseParams &P, int tile, hipStream_t st) {
+    const dim3 grid((unsigned)(P.tiles_m * P.tiles_n), (unsigned)P.splits);
+    if (tile == DN_TILE_256)
+        hipLaunchKernelGGL((k_dense<256, 256, 2, 4, FORM, EPI>), grid, dim3(512), 0, st, P);
+    else
+        hipLaunchKernelGGL((k_dense<128, 128, 2, 2, FORM, EPI>), grid, dim3(256), 0, st, P);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || P.splits == 1) return e;
+    const int64_t work = (int64_t)P.M * (P.N / 8);
+    const int64_t blocks = (work + 255) / 256;
+    hipLaunchKernelGGL((k_dense_join<EPI>), dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, st, P);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,404 @@
+// moe_dense.hip -- the C ABI of the dense operators (linear and the gated
+// feed-forward block, forward and backward; include/moe.h): host-side
+// validation, workspace layout, tile and split choice, launches.  They stand
+// next to the routed layer: the dense parts of the same model in bf16 (a
+// shared expert kept in 16 bits, dense layers, projections).
+#include <hip/hip_runtime.h>
+#include <string.h>
+
+#include "../../include/moe.h"
+#include "moe_internal.h"
+
+namespace moe {
+hipError_t dense_split3_launch(const float *x, uint16_t *out, int64_t n, hipStream_t st);
+hipError_t dense_dz_launch(const DzParams &P, hipStream_t st);
+hipError_t dense_colsum_launch(const ColsumParams &P, hipStream_t st);
+hipError_t dense_linear_launch(const DenseParams &P, int tile, hipStream_t st);
+hipError_t dense_gated_launch(const DenseParams &P, int tile, hipStream_t st);
+hipError_t dense_dgated_launch(const DenseParams &P, int tile, hipStream_t st);
+hipError_t dense_dx_launch(const DenseParams &P, int tile, hipStream_t st);
+hipError_t dense_dw_launch(const DenseParams &P, int tile, hipStream_t st);
+}  // namespace moe
+
+using namespace moe;
+
+static_assert(DN_ACT_NONE == MOE_ACT_NONE && DN_ACT_SILU == MOE_ACT_SILU && DN_ACT_GELU == MOE_ACT_GELU &&
+                  DN_ACT_GELU_TANH == MOE_ACT_GELU_TANH && DN_ACT_RELU == MOE_ACT_RELU,
+              "activation codes");
+
+namespace {
+
+constexpr int DN_MAX_WIDTH = 1 << 20;
+constexpr int DN_MAX_ROWS = 1 << 24;
+constexpr int DN_SPLIT_TILES = 512;  // tiles of a split product over all its splits
+constexpr int DN_DZ_CHUNKS = 256;  // row chunks of the bias gradient
+
+int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int check_width(int32_t a, int32_t b) {
+    if (a <= 0 || b <= 0) return MOE_ERR_INVALID_ARG;
+    if (a % 8 || b % 8 || a > DN_MAX_WIDTH || b > DN_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+int check_rows(int32_t T) {
+    if (T < 0) return MOE_ERR_INVALID_ARG;
+    return T > DN_MAX_ROWS ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+bool valid_dtype(int d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16; }
+bool valid_act(int a) { return a >= MOE_ACT_NONE && a <= MOE_ACT_RELU; }
+bool misaligned(const void *p) { return ((uintptr_t)p & 15) != 0; }
+
+// ---- tile and split choice ----
+struct Plan {
+    int tile, tiles_m, tiles_n, splits, per;
+};
+// C of M x N columns of the weight side (gated: 2F) over `steps` 64-k steps
+Plan make_plan(int64_t M, int64_t N, int64_t steps) {
+    Plan p;
+    const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256);
+    p.tile = t256 >= 192 ? DN_TILE_256 : DN_TILE_128;
+    const int bt = p.tile == DN_TILE_256 ? 256 : 128;
+    p.tiles_m = (int)ceil_div(M, bt);
+    p.tiles_n = (int)ceil_div(N, bt);
+    const int64_t tiles = max64((int64_t)p.tiles_m * p.tiles_n, 1);  // (M = 0: nothing is launched)
+    int64_t s = p.tile == DN_TILE_256 ? 1 : DN_SPLIT_TILES / tiles;
+    if (s > steps / 4) s = steps / 4;
+    if (s < 1) s = 1;
+    p.per = (int)ceil_div(steps > 0 ? steps : 1, s);
+    p.splits = (int)ceil_div(steps > 0 ? steps : 1, p.per);
+    return p;
+}
+int64_t ksteps(int64_t K) { return ceil_div(K, DN_BK); }
+
+struct Carve {  // workspace regions after the head
+    int64_t off = (int64_t)align_up(COUNTER_WORDS * 4, 256);
+    int64_t take(int64_t bytes) {
+        const int64_t a = off;
+        off += (int64_t)align_up((size_t)bytes, 256);
+        return a;
+    }
+};
+uint8_t *at(void *ws, int64_t off) { return (uint8_t *)ws + off; }
+
+void set_plan(DenseParams &P, const Plan &p, int M, int N, int steps, float *part) {
+    P.M = M;
+    P.N = N;
+    P.steps = steps;
+    P.tiles_m = p.tiles_m;
+    P.tiles_n = p.tiles_n;
+    P.splits = p.splits;
+    P.steps_per_split = p.per;
+    P.part = part;
+}
+// The parts of a split product: at most DN_SPLIT_TILES tiles of 128 x 128
+// over all splits, whatever the sizes; a fixed region, so that a workspace
+// sized for T rows also serves fewer.
+constexpr int64_t DN_PART_BYTES = (int64_t)DN_SPLIT_TILES * 128 * 128 * 4;
+
+// ---- workspace layouts ----
+struct LinearWs {
+    int64_t x3, part, total;         // forward
+    int64_t dz, chunks, bpart, btotal;  // backward
+    Plan fwd, dx, dw;
+};
+LinearWs linear_ws(int64_t T, int64_t K, int64_t N, bool x_f32) {
+    LinearWs w;
+    w.fwd = make_plan(T, N, ksteps(K) * (x_f32 ? 3 : 1));
+    w.dx = make_plan(T, K, ksteps(N));
+    w.dw = make_plan(N, K, ksteps(T));
+    Carve c;
+    w.x3 = c.take(x_f32 ? T * K * 6 : 0);
+    w.part = c.take(DN_PART_BYTES);
+    w.total = c.off;
+    Carve b;
+    w.dz = b.take(T * N * 2);
+    w.chunks = b.take((int64_t)DN_DZ_CHUNKS * N * 4);
+    w.bpart = b.take(DN_PART_BYTES);
+    w.btotal = b.off;
+    return w;
+}
+struct GatedWs {
+    int64_t x3, h, part, total;
+    int64_t dgu, bh, bpart, btotal;
+    Plan gu, down, dh, dx, dw, dd;
+};
+GatedWs gated_ws(int64_t T, int64_t H, int64_t F, bool x_f32, bool y_f32) {
+    GatedWs w;
+    w.gu = make_plan(T, 2 * F, ksteps(H) * (x_f32 ? 3 : 1));
+    w.down = make_plan(T, H, ksteps(F) * (y_f32 ? 3 : 1));
+    w.dh = make_plan(T, F, ksteps(H));
+    w.dx = make_plan(T, H, 2 * ksteps(F));
+    w.dw = make_plan(2 * F, H, ksteps(T));
+    w.dd = make_plan(H, F, ksteps(T));
+    Carve c;
+    w.x3 = c.take(x_f32 ? T * H * 6 : 0);
+    w.h = c.take(T * F * 2 * (y_f32 ? 3 : 1));
+    w.part = c.take(DN_PART_BYTES);
+    w.total = c.off;
+    Carve b;
+    w.dgu = b.take(T * F * 4);
+    w.bh = b.take(T * F * 2);
+    w.bpart = b.take(DN_PART_BYTES);
+    w.btotal = b.off;
+    return w;
+}
+
+inline hipStream_t S(int64_t s) { return (hipStream_t)(intptr_t)s; }
+int launch_err(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
+
+// x's products with rows of K: one (bf16) or three (fp32, its exact bf16
+// terms, written to x3 first)
+int x_segments(DenseParams &P, const void *x, bool x_f32, int64_t T, int64_t K, uint16_t *x3, hipStream_t st) {
+    if (x_f32 && dense_split3_launch((const float *)x, x3, T * K, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    P.nseg = x_f32 ? 3 : 1;
+    for (int i = 0; i < P.nseg; ++i) {
+        P.seg[i].a = x_f32 ? x3 + (int64_t)i * T * K : (const uint16_t *)x;
+        P.seg[i].lda = K;
+        P.seg[i].K = (int)K;
+    }
+    return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t moe_linear_workspace_bytes(int32_t T, int32_t in, int32_t out) {
+    int rc = check_rows(T);
+    if (rc) return rc;
+    if ((rc = check_width(in, out))) return rc;
+    const LinearWs a = linear_ws(T, in, out, false), b = linear_ws(T, in, out, true);
+    return max64(max64(a.total, b.total), a.btotal);
+}
+
+int moe_linear(const void *x, int32_t x_dtype, int32_t T, int32_t in, const void *w, int32_t out, const void *bias,
+               int32_t act, const void *residual, int32_t r_dtype, void *z, void *y, int32_t y_dtype, void *ws,
+               int64_t ws_bytes, int64_t stream) {
+    if (T != 0 && (!x || !w || !y || !ws)) return MOE_ERR_INVALID_ARG;
+    if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype) || !valid_act(act)) return MOE_ERR_INVALID_ARG;
+    if (residual && !valid_dtype(r_dtype)) return MOE_ERR_INVALID_ARG;
+    if (misaligned(x) || misaligned(w) || misaligned(bias) || misaligned(residual) || misaligned(z) || misaligned(y) ||
+        misaligned(ws))
+        return MOE_ERR_INVALID_ARG;
+    int rc = check_rows(T);
+    if (rc) return rc;
+    if ((rc = check_width(in, out))) return rc;
+    if (T == 0) return MOE_OK;
+    const bool xf = x_dtype == MOE_DTYPE_F32;
+    const LinearWs L = linear_ws(T, in, out, xf);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    int cus;
+    if ((rc = device_cus(cus))) return rc;
+    DenseParams P;
+    memset(&P, 0, sizeof(P));
+    if ((rc = x_segments(P, x, xf, T, in, (uint16_t *)at(ws, L.x3), S(stream)))) return rc;
+    for (int i = 0; i < P.nseg; ++i) {
+        P.seg[i].b = (const uint16_t *)w;
+        P.seg[i].ldb = in;
+    }
+    set_plan(P, L.fwd, T, out, (int)(ksteps(in) * P.nseg), (float *)at(ws, L.part));
+    P.e.bias = (const uint16_t *)bias;
+    P.e.res = residual;
+    P.e.res_f32 = r_dtype == MOE_DTYPE_F32;
+    P.e.y = y;
+    P.e.y_f32 = y_dtype == MOE_DTYPE_F32;
+    P.e.z = (uint16_t *)z;
+    P.e.act = act;
+    return launch_err(dense_linear_launch(P, L.fwd.tile, S(stream)));
+}
+
+int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, const void *x, const void *w, const void *z,
+                        int32_t act, void *dx, void *dw, void *dbias, int32_t dw_dtype, int32_t accumulate, void *ws,
+                        int64_t ws_bytes, int64_t stream) {
+    if (!dx && !dw && !dbias) return MOE_ERR_INVALID_ARG;
+    if (T != 0 && (!dy || (dx && !w) || (dw && !x))) return MOE_ERR_INVALID_ARG;
+    if (!valid_act(act) || !valid_dtype(dw_dtype) || !ws) return MOE_ERR_INVALID_ARG;
+    if (T != 0 && act != MOE_ACT_NONE && !z) return MOE_ERR_INVALID_ARG;
+    if (misaligned(dy) || misaligned(x) || misaligned(w) || misaligned(z) || misaligned(dx) || misaligned(dw) ||
+        misaligned(dbias) || misaligned(ws))
+        return MOE_ERR_INVALID_ARG;
+    int rc = check_rows(T);
+    if (rc) return rc;
+    if ((rc = check_width(in, out))) return rc;
+    const LinearWs L = linear_ws(T, in, out, false);
+    if (ws_bytes < L.btotal) return MOE_ERR_WORKSPACE;
+    int cus;
+    if ((rc = device_cus(cus))) return rc;
+    const hipStream_t st = S(stream);
+    const bool with_act = act != MOE_ACT_NONE;
+    const uint16_t *dz = with_act ? (const uint16_t *)at(ws, L.dz) : (const uint16_t *)dy;
+    int nchunks = 0;
+    if (T != 0 && (with_act || dbias)) {
+        DzParams D;
+        memset(&D, 0, sizeof(D));
+        D.dy = (const uint16_t *)dy;
+        D.z = with_act ? (const uint16_t *)z : nullptr;
+        D.dz = with_act && (dx || dw) ? (uint16_t *)at(ws, L.dz) : nullptr;
+        D.part = dbias ? (float *)at(ws, L.chunks) : nullptr;
+        D.T = T;
+        D.N = out;
+        D.act = act;
+        // chunks of at least 16 rows, at most DN_DZ_CHUNKS of them
+        D.rows_per_chunk = max64(ceil_div(T, DN_DZ_CHUNKS), 16);
+        nchunks = D.nchunks = (int)ceil_div(T, D.rows_per_chunk);
+        if (dense_dz_launch(D, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    if (dbias) {
+        ColsumParams C{(const float *)at(ws, L.chunks), dbias, out, nchunks, dw_dtype == MOE_DTYPE_F32, accumulate != 0};
+        if (dense_colsum_launch(C, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    if (dx && T != 0) {
+        DenseParams P;
+        memset(&P, 0, sizeof(P));
+        P.nseg = 1;
+        P.seg[0] = DenseSeg{dz, (const uint16_t *)w, nullptr, out, in, out};
+        set_plan(P, L.dx, T, in, (int)ksteps(out), (float *)at(ws, L.bpart));
+        P.e.y = dx;
+        if (dense_dx_launch(P, L.dx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    if (dw) {
+        DenseParams P;
+        memset(&P, 0, sizeof(P));
+        P.nseg = 1;
+        P.seg[0] = DenseSeg{dz, (const uint16_t *)x, nullptr, out, in, T};
+        set_plan(P, L.dw, out, in, (int)ksteps(T), (float *)at(ws, L.bpart));
+        P.e.y = dw;
+        P.e.m_split = out;
+        P.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
+        P.e.accumulate = accumulate != 0;
+        if (dense_dw_launch(P, L.dw.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    return MOE_OK;
+}
+
+int64_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t hidden, int32_t ffn) {
+    int rc = check_rows(T);
+    if (rc) return rc;
+    if ((rc = check_width(hidden, ffn))) return rc;
+    int64_t n = gated_ws(T, hidden, ffn, false, false).btotal;
+    for (int i = 0; i < 4; ++i) n = max64(n, gated_ws(T, hidden, ffn, i & 1, i >> 1).total);
+    return n;
+}
+
+int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn *w, const void *residual, int32_t r_dtype,
+                  void *gu, void *y, int32_t y_dtype, void *ws, int64_t ws_bytes, int64_t stream) {
+    if (!w) return MOE_ERR_INVALID_ARG;
+    if (T != 0 && (!x || !y || !ws || !w->gate || !w->up || !w->down)) return MOE_ERR_INVALID_ARG;
+    if (!valid_dtype(x_dtype) || !valid_dtype(y_dtype) || !valid_act(w->act)) return MOE_ERR_INVALID_ARG;
+    if (residual && !valid_dtype(r_dtype)) return MOE_ERR_INVALID_ARG;
+    if (misaligned(x) || misaligned(w->gate) || misaligned(w->up) || misaligned(w->down) || misaligned(residual) ||
+        misaligned(gu) || misaligned(y) || misaligned(ws))
+        return MOE_ERR_INVALID_ARG;
+    int rc = check_rows(T);
+    if (rc) return rc;
+    const int H = w->hidden, F = w->ffn;
+    if ((rc = check_width(H, F))) return rc;
+    if (T == 0) return MOE_OK;
+    const bool xf = x_dtype == MOE_DTYPE_F32, yf = y_dtype == MOE_DTYPE_F32;
+    const GatedWs L = gated_ws(T, H, F, xf, yf);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    int cus;
+    if ((rc = device_cus(cus))) return rc;
+    const hipStream_t st = S(stream);
+    uint16_t *h = (uint16_t *)at(ws, L.h);
+    DenseParams P;
+    memset(&P, 0, sizeof(P));
+    if ((rc = x_segments(P, x, xf, T, H, (uint16_t *)at(ws, L.x3), st))) return rc;
+    for (int i = 0; i < P.nseg; ++i) {
+        P.seg[i].b = (const uint16_t *)w->gate;
+        P.seg[i].b2 = (const uint16_t *)w->up;
+        P.seg[i].ldb = H;
+    }
+    set_plan(P, L.gu, T, F, (int)(ksteps(H) * P.nseg), (float *)at(ws, L.part));
+    P.e.act = w->act;
+    P.e.h = h;
+    P.e.h_terms = yf ? 3 : 1;
+    P.e.gu = (uint16_t *)gu;
+    if (dense_gated_launch(P, L.gu.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    DenseParams D;
+    memset(&D, 0, sizeof(D));
+    D.nseg = yf ? 3 : 1;
+    for (int i = 0; i < D.nseg; ++i)
+        D.seg[i] = DenseSeg{h + (int64_t)i * T * F, (const uint16_t *)w->down, nullptr, F, F, F};
+    set_plan(D, L.down, T, H, (int)(ksteps(F) * D.nseg), (float *)at(ws, L.part));
+    D.e.res = residual;
+    D.e.res_f32 = r_dtype == MOE_DTYPE_F32;
+    D.e.y = y;
+    D.e.y_f32 = yf;
+    return launch_err(dense_linear_launch(D, L.down.tile, st));
+}
+
+int moe_gated_ffn_backward(const void *dy, const void *x, int32_t T, const moe_dense_ffn *w, const void *gu, void *dx,
+                           void *dgate, void *dup, void *ddown, int32_t dw_dtype, int32_t accumulate, void *ws,
+                           int64_t ws_bytes, int64_t stream) {
+    if (!w || !ws) return MOE_ERR_INVALID_ARG;
+    if (!dx && !dgate && !dup && !ddown) return MOE_ERR_INVALID_ARG;
+    if (T != 0 && (!dy || !gu || !w->down || ((dgate || dup) && !x) || (dx && (!w->gate || !w->up))))
+        return MOE_ERR_INVALID_ARG;
+    if (!valid_dtype(dw_dtype) || !valid_act(w->act)) return MOE_ERR_INVALID_ARG;
+    if (misaligned(dy) || misaligned(x) || misaligned(w->gate) || misaligned(w->up) || misaligned(w->down) ||
+        misaligned(gu) || misaligned(dx) || misaligned(dgate) || misaligned(dup) || misaligned(ddown) || misaligned(ws))
+        return MOE_ERR_INVALID_ARG;
+    int rc = check_rows(T);
+    if (rc) return rc;
+    const int H = w->hidden, F = w->ffn;
+    if ((rc = check_width(H, F))) return rc;
+    const GatedWs L = gated_ws(T, H, F, false, false);
+    if (ws_bytes < L.btotal) return MOE_ERR_WORKSPACE;
+    int cus;
+    if ((rc = device_cus(cus))) return rc;
+    const hipStream_t st = S(stream);
+    uint16_t *dgu = (uint16_t *)at(ws, L.dgu), *h = (uint16_t *)at(ws, L.bh);
+    float *part = (float *)at(ws, L.bpart);
+    if (T != 0) {  // dh = dy Wd, then dg, du and h
+        DenseParams P;
+        memset(&P, 0, sizeof(P));
+        P.nseg = 1;
+        P.seg[0] = DenseSeg{(const uint16_t *)dy, (const uint16_t *)w->down, nullptr, H, F, H};
+        set_plan(P, L.dh, T, F, (int)ksteps(H), part);
+        P.e.act = w->act;
+        P.e.gu_in = (const uint16_t *)gu;
+        P.e.dgu = dgu;
+        P.e.h = ddown ? h : nullptr;
+        if (dense_dgated_launch(P, L.dh.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    if (dx && T != 0) {  // dx = dg Wg + du Wu
+        DenseParams P;
+        memset(&P, 0, sizeof(P));
+        P.nseg = 2;
+        P.seg[0] = DenseSeg{dgu, (const uint16_t *)w->gate, nullptr, 2 * (int64_t)F, H, F};
+        P.seg[1] = DenseSeg{dgu + F, (const uint16_t *)w->up, nullptr, 2 * (int64_t)F, H, F};
+        set_plan(P, L.dx, T, H, (int)(2 * ksteps(F)), part);
+        P.e.y = dx;
+        if (dense_dx_launch(P, L.dx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    if (dgate || dup) {  // [dg du]^T x
+        DenseParams P;
+        memset(&P, 0, sizeof(P));
+        P.nseg = 1;
+        P.seg[0] = DenseSeg{dgu, (const uint16_t *)x, nullptr, 2 * (int64_t)F, H, T};
+        set_plan(P, L.dw, 2 * F, H, (int)ksteps(T), part);
+        P.e.y = dgate;
+        P.e.y2 = dup;
+        P.e.m_split = F;
+        P.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
+        P.e.accumulate = accumulate != 0;
+        if (dense_dw_launch(P, L.dw.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    if (ddown) {  // dy^T h
+        DenseParams P;
+        memset(&P, 0, sizeof(P));
+        P.nseg = 1;
+        P.seg[0] = DenseSeg{(const uint16_t *)dy, h, nullptr, H, F, T};
+        set_plan(P, L.dd, H, F, (int)ksteps(T), part);
+        P.e.y = ddown;
+        P.e.m_split = H;
+        P.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
+        P.e.accumulate = accumulate != 0;
+        if (dense_dw_launch(P, L.dd.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -265,6 +265,75 @@ struct PrepareParams {
     int n_experts, H, nc, bb;  // nc = F / 32 (down blocks per row), bb = bytes per block
 };
 
+// Head of every workspace: after the slot and slice counters the error word
+// (a line of its own), then the per-workgroup epochs.
+constexpr size_t COUNTER_WORDS = (size_t)(2 * DEC_MAX_SLOTS + DEC_MAX_SLICES + 1) * DEC_CSTRIDE + EPOCH_SLOTS;
+
+// The current device's compute units (a MOE_* status).
+int device_cus(int &cus);
+
+// ---------------------------------------------------------------------------
+// Dense products (bf16 weights): linear and the gated feed-forward block.
+// ---------------------------------------------------------------------------
+constexpr int DN_BK = 64;        // k per step of the main loop
+constexpr int DN_MAX_SEG = 3;    // products summed into one output
+
+// activations (MOE_ACT_* of the interface)
+enum DenseAct { DN_ACT_NONE = 0, DN_ACT_SILU = 1, DN_ACT_GELU = 2, DN_ACT_GELU_TANH = 3, DN_ACT_RELU = 4 };
+
+// One product of the sum: A [M][K] and B [N][K] or their transposes (which, is
+// the kernel's type), row strides in elements.
+struct DenseSeg {
+    const uint16_t *a, *b, *b2;  // b2: the up projection of a gated product
+    int64_t lda, ldb;
+    int K;
+};
+
+// What becomes of the sums (see the epilogues in moe_dense.h).
+struct DenseEpi {
+    const uint16_t *bias;  // [N] or null
+    const void *res;       // [M][N] or null
+    void *y;               // [M][N]
+    void *y2;              // weight gradients: the rows from m_split on
+    uint16_t *z;           // [M][N] pre-activation or null
+    uint16_t *h;           // gated: h_terms planes of [M][N]
+    uint16_t *gu;          // gated: [M][2N] gate and up, kept (or null)
+    const uint16_t *gu_in;  // gated backward: the kept gate and up
+    uint16_t *dgu;          // gated backward: their gradients [M][2N]
+    int m_split;
+    int act, y_f32, res_f32, h_terms, accumulate;
+};
+
+struct DenseParams {
+    DenseSeg seg[DN_MAX_SEG];
+    DenseEpi e;
+    float *part;      // split products: [splits][M][N] fp32 (gated: [splits][M][2N])
+    int nseg, steps;  // 64-k steps over all products of the sum
+    int M, N;         // output rows and columns (gated: N = F)
+    int tiles_m, tiles_n;
+    int splits, steps_per_split;
+};
+
+// product forms: C = A B^T (rows of both run along k), C = A B (B's rows run
+// along n), C = A^T B (rows of A run along m, of B along n)
+enum DenseForm { DN_NT = 0, DN_NN = 1, DN_TN = 2 };
+enum DenseEpiKind { DN_EPI_LINEAR = 0, DN_EPI_GATED = 1, DN_EPI_DGATED = 2, DN_EPI_GRAD = 3 };
+enum DenseTile { DN_TILE_128 = 0, DN_TILE_256 = 1 };
+
+// dz = dy * act'(z) and the column sums of dz over row chunks
+struct DzParams {
+    const uint16_t *dy, *z;  // [T][N]; z null: no activation
+    uint16_t *dz;            // [T][N] or null
+    float *part;             // [nchunks][N] or null
+    int64_t rows_per_chunk;
+    int T, N, nchunks, act;
+};
+struct ColsumParams {
+    const float *part;  // [nchunks][N]
+    void *out;          // [N]
+    int N, nchunks, out_f32, accumulate;
+};
+
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 }  // namespace moe

@@ -27,10 +27,13 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 PATH_AUTO, PATH_DECODE, PATH_PREFILL = 0, 1, 2
 DECODE_MAX_ROWS = 16
 LAYOUT_ROWS, LAYOUT_PREPARED = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = 0, 1, 2, 3, 4
 
 EXPORTS = ["moe_version", "moe_status_string", "moe_expert_bytes", "moe_workspace_bytes",
            "moe_prepare_qweights", "moe_workspace_error", "moe_router_logits", "moe_route", "moe_group", "moe_expert_ffn",
-           "moe_layer_forward", "moe_layer_forward_noalloc"]
+           "moe_layer_forward", "moe_layer_forward_noalloc",
+           "moe_linear_workspace_bytes", "moe_linear", "moe_linear_backward",
+           "moe_gated_ffn_workspace_bytes", "moe_gated_ffn", "moe_gated_ffn_backward"]
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 # bits of the workspace error word (moe_workspace_error)
@@ -49,6 +52,13 @@ class QWeights(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("bits", ctypes.c_int32), ("n_experts", ctypes.c_int32),
                 ("hidden", ctypes.c_int32), ("ffn", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("down_bits", ctypes.c_int32), ("codebook", ctypes.c_int8 * 16)]
+
+
+class DenseFFN(ctypes.Structure):
+    """moe_dense_ffn: device pointers, sizes and activation of a dense gated
+    feed-forward block (see dense_ffn, which keeps the tensors alive)."""
+    _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("down", ctypes.c_void_p),
+                ("hidden", ctypes.c_int32), ("ffn", ctypes.c_int32), ("act", ctypes.c_int32)]
 
 
 BITS_NL4 = 20  # the non-linear 4-bit format (4-bit layout, codes index a 16-entry int8 table)
@@ -101,6 +111,19 @@ def lib():
         L.moe_layer_forward_noalloc.restype = ctypes.c_int
         L.moe_layer_forward_noalloc.argtypes = [vp, i32, vp, i32, i32, ctypes.POINTER(QWeights),
                                                 ctypes.POINTER(QWeights), vp, vp, vp, vp, i32, i64]
+        ffn = ctypes.POINTER(DenseFFN)
+        L.moe_linear_workspace_bytes.restype = i64
+        L.moe_linear_workspace_bytes.argtypes = [i32] * 3
+        L.moe_linear.restype = ctypes.c_int
+        L.moe_linear.argtypes = [vp, i32, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, i32, vp, i64, i64]
+        L.moe_linear_backward.restype = ctypes.c_int
+        L.moe_linear_backward.argtypes = [vp, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp, i32, i32, vp, i64, i64]
+        L.moe_gated_ffn_workspace_bytes.restype = i64
+        L.moe_gated_ffn_workspace_bytes.argtypes = [i32] * 3
+        L.moe_gated_ffn.restype = ctypes.c_int
+        L.moe_gated_ffn.argtypes = [vp, i32, i32, ffn, vp, i32, vp, vp, i32, vp, i64, i64]
+        L.moe_gated_ffn_backward.restype = ctypes.c_int
+        L.moe_gated_ffn_backward.argtypes = [vp, vp, i32, ffn, vp, vp, vp, vp, vp, i32, i32, vp, i64, i64]
         _lib = L
     return _lib
 
@@ -260,3 +283,172 @@ def layer_forward_noalloc(x: torch.Tensor, logits: torch.Tensor, k: int, routed:
                                            _ptr(topk_idx), _ptr(topk_w), _ptr(heat), path, _stream(stream)),
            "moe_layer_forward_noalloc")
     return y
+
+
+# ---------------------------------------------------------------------------
+# Dense operators (bf16 weights): linear and the gated feed-forward block
+# ---------------------------------------------------------------------------
+_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+
+
+def _dense(name: str, t, shape: tuple, dtypes: tuple, dev: torch.device, optional: bool = True):
+    """Checks an operand of a dense operator; returns (address, type code)."""
+    if t is None:
+        if optional:
+            return None, DTYPE_F32
+        raise TypeError(f"{name} is required")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other operands on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), _CODES[t.dtype]
+
+
+_ANY, _BF16 = (torch.float32, torch.bfloat16), (torch.bfloat16,)
+
+
+def _dense_device(x: torch.Tensor, ws: torch.Tensor) -> torch.device:
+    """The operands' device: a GPU, the current one (launches go there)."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("dense operators take device tensors")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"operands on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    return dev
+
+
+def _dense_new(shape: tuple, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+    """A new output, allocated for the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def linear_workspace_bytes(T: int, inner: int, outer: int) -> int:
+    n = int(lib().moe_linear_workspace_bytes(T, inner, outer))
+    if n < 0:
+        raise MoeError(n, "moe_linear_workspace_bytes")
+    return n
+
+
+def linear_workspace(T: int, inner: int, outer: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for linear and linear_backward, up to T rows."""
+    return torch.zeros(linear_workspace_bytes(T, inner, outer), dtype=torch.uint8, device=device)
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, bias=None, act: int = ACT_NONE, residual=None, z=None,
+           y=None, stream=None) -> torch.Tensor:
+    """y = act(x w^T + bias) + residual.  x [T, in] fp32/bf16, w [out, in]
+    bf16, bias [out] bf16, residual and y [T, out] fp32/bf16 (y: x's type
+    unless given; y may be the residual).  z: bf16 [T, out], receives the
+    pre-activation for linear_backward."""
+    dev = _dense_device(x, ws)
+    T, K = x.shape
+    N = w.shape[0]
+    if y is None:
+        y = _dense_new((T, N), x.dtype, dev, stream)
+    px, xc = _dense("x", x, (T, K), _ANY, dev)
+    pw, _ = _dense("w", w, (N, K), _BF16, dev)
+    pb, _ = _dense("bias", bias, (N,), _BF16, dev)
+    pr, rc = _dense("residual", residual, (T, N), _ANY, dev)
+    pz, _ = _dense("z", z, (T, N), _BF16, dev)
+    py, yc = _dense("y", y, (T, N), _ANY, dev)
+    _check(lib().moe_linear(px, xc, T, K, pw, N, pb, act, pr, rc, pz, py, yc, ws.data_ptr(), ws.numel(), _stream(stream)),
+           "moe_linear")
+    return y
+
+
+def linear_backward(dy: torch.Tensor, x, w, ws: torch.Tensor, z=None, act: int = ACT_NONE, dx=None, dw=None, dbias=None,
+                    accumulate: bool = False, stream=None) -> None:
+    """Gradients of linear into the given tensors: dx [T, in] bf16 (needs w),
+    dw [out, in] (needs x) and dbias [out] fp32/bf16 of one type; with
+    accumulate, dw and dbias are added to.  dy [T, out], x, w bf16; z as
+    linear wrote it (needed with an activation)."""
+    dev = _dense_device(dy, ws)
+    T, N = dy.shape
+    K = next((t.shape[-1] for t in (dx, dw, x, w) if t is not None), 8)
+    pd, _ = _dense("dy", dy, (T, N), _BF16, dev)
+    px, _ = _dense("x", x, (T, K), _BF16, dev, optional=dw is None)
+    pw, _ = _dense("w", w, (N, K), _BF16, dev, optional=dx is None)
+    pz, _ = _dense("z", z, (T, N), _BF16, dev, optional=act == ACT_NONE)
+    pdx, _ = _dense("dx", dx, (T, K), _BF16, dev)
+    pdw, wc = _dense("dw", dw, (N, K), _ANY, dev)
+    pdb, bc = _dense("dbias", dbias, (N,), _ANY, dev)
+    if dw is not None and dbias is not None and wc != bc:
+        raise TypeError("dw and dbias must have one type")
+    _check(lib().moe_linear_backward(pd, T, K, N, px, pw, pz, act, pdx, pdw, pdb, bc if dw is None else wc, int(accumulate),
+                                     ws.data_ptr(), ws.numel(), _stream(stream)), "moe_linear_backward")
+
+
+def dense_ffn(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, act: int = ACT_SILU) -> DenseFFN:
+    """Describe a dense gated feed-forward block: gate, up [ffn, hidden] and
+    down [hidden, ffn], bf16 device tensors (kept alive by the result)."""
+    F, H = gate.shape
+    pg, _ = _dense("gate", gate, (F, H), _BF16, gate.device)
+    pu, _ = _dense("up", up, (F, H), _BF16, gate.device)
+    pd, _ = _dense("down", down, (H, F), _BF16, gate.device)
+    d = DenseFFN(pg, pu, pd, H, F, act)
+    d.tensors = (gate, up, down)
+    return d
+
+
+def gated_ffn_workspace_bytes(T: int, hidden: int, ffn: int) -> int:
+    n = int(lib().moe_gated_ffn_workspace_bytes(T, hidden, ffn))
+    if n < 0:
+        raise MoeError(n, "moe_gated_ffn_workspace_bytes")
+    return n
+
+
+def gated_ffn_workspace(T: int, hidden: int, ffn: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for gated_ffn and gated_ffn_backward, up to T rows."""
+    return torch.zeros(gated_ffn_workspace_bytes(T, hidden, ffn), dtype=torch.uint8, device=device)
+
+
+def gated_ffn(x: torch.Tensor, ffn: DenseFFN, ws: torch.Tensor, residual=None, gu=None, y=None, stream=None) -> torch.Tensor:
+    """y = (act(x gate^T) * (x up^T)) down^T + residual.  x [T, hidden],
+    residual and y [T, hidden] fp32/bf16 (y: x's type unless given; y may be
+    the residual).  gu: bf16 [T, 2*ffn], receives gate and up for
+    gated_ffn_backward."""
+    dev = _dense_device(x, ws)
+    T = x.shape[0]
+    H, F = ffn.hidden, ffn.ffn
+    if y is None:
+        y = _dense_new((T, H), x.dtype, dev, stream)
+    px, xc = _dense("x", x, (T, H), _ANY, dev)
+    pr, rc = _dense("residual", residual, (T, H), _ANY, dev)
+    pg, _ = _dense("gu", gu, (T, 2 * F), _BF16, dev)
+    py, yc = _dense("y", y, (T, H), _ANY, dev)
+    _check(lib().moe_gated_ffn(px, xc, T, ctypes.byref(ffn), pr, rc, pg, py, yc, ws.data_ptr(), ws.numel(),
+                               _stream(stream)), "moe_gated_ffn")
+    return y
+
+
+def gated_ffn_backward(dy: torch.Tensor, x, gu: torch.Tensor, ffn: DenseFFN, ws: torch.Tensor, dx=None, dgate=None,
+                       dup=None, ddown=None, accumulate: bool = False, stream=None) -> None:
+    """Gradients of gated_ffn into the given tensors: dx [T, hidden] bf16,
+    dgate, dup [ffn, hidden] and ddown [hidden, ffn] fp32/bf16 of one type;
+    with accumulate, the weight gradients are added to.  dy, x [T, hidden]
+    bf16 (x is needed for dgate and dup); gu as gated_ffn wrote it."""
+    dev = _dense_device(dy, ws)
+    T = dy.shape[0]
+    H, F = ffn.hidden, ffn.ffn
+    pd, _ = _dense("dy", dy, (T, H), _BF16, dev)
+    px, _ = _dense("x", x, (T, H), _BF16, dev, optional=dgate is None and dup is None)
+    pg, _ = _dense("gu", gu, (T, 2 * F), _BF16, dev, optional=False)
+    pdx, _ = _dense("dx", dx, (T, H), _BF16, dev)
+    grads = [_dense("dgate", dgate, (F, H), _ANY, dev), _dense("dup", dup, (F, H), _ANY, dev),
+             _dense("ddown", ddown, (H, F), _ANY, dev)]
+    codes = {c for p, c in grads if p is not None}
+    if len(codes) > 1:
+        raise TypeError("dgate, dup and ddown must have one type")
+    _check(lib().moe_gated_ffn_backward(pd, px, T, ctypes.byref(ffn), pg, pdx, grads[0][0], grads[1][0], grads[2][0],
+                                        codes.pop() if codes else DTYPE_F32, int(accumulate), ws.data_ptr(), ws.numel(),
+                                        _stream(stream)), "moe_gated_ffn_backward")
