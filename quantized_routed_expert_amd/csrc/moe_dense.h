@@ -37,9 +37,19 @@ typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
 
 constexpr uint32_t DN_OOB = 0x80000000u;  // past every buffer's range (< 2^31 bytes)
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t dn_rsrc(const void *p, int64_t bytes) {
-    const int n = bytes <= 0 ? 0 : (bytes > 0x7FFFFFFF ? 0x7FFFFFFF : (int)bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, n, 0x00027000);
+// Buffer of `bytes` bytes from p (raw, stride 0): loads past it return zero.
+__device__ __forceinline__ u32x4 dn_rsrc(const void *p, int bytes) {
+    const uint64_t a = (uint64_t)p;
+    return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, (uint32_t)max(bytes, 0), 0x00027000u};
+}
+// 16 bytes per lane from buffer offset `off` to LDS: lane l writes dst + 16 l.
+// Counts in vmcnt.  As an instruction of its own and not the builtin: with
+// that, the compiler waits for all such loads before every transposed LDS
+// read, though they go to the other buffer.  It has no register result; LDS
+// is read only after wait_vm and a barrier.
+__device__ __forceinline__ void dn_load_lds(u32x4 rsrc, uint32_t dst, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(dst), "v"(off), "s"(rsrc)
+                 : "memory", "m0");
 }
 
 // ---------------------------------------------------------------------------
@@ -276,15 +286,23 @@ struct DnStream {
     static constexpr int NL = R * 128 / 1024 / NW;  // loads per wave and step
     static constexpr int BYTES = R * 128;
     static_assert(R * 128 % (1024 * NW) == 0, "whole wave loads");
+    static_assert(!KC || SH == 2 || (8 * NW) % (2 << SH) == 0, "one piece for all of a lane's rows");
     uint32_t voff[NL];
+    int kpiece;  // k-rows: the first k of the 16-byte piece that this lane loads of each of its rows
 
-    // ld in elements; cols: columns left from the tile's first (transposed)
-    __device__ __forceinline__ void setup(int wave, int lane, int64_t ld, int64_t cols) {
+    // row of the tile whose piece (k-rows) the lane loads with load j
+    __device__ __forceinline__ static int row(int j, int wave, int lane) { return (j * NW + wave) * 8 + (lane >> 3); }
+    // ld in elements; cols: columns left from the tile's first (transposed).
+    // gated: the tile's 64-row groups hold 32 rows of one matrix, then the
+    // same 32 rows of another
+    __device__ __forceinline__ void setup(int wave, int lane, int64_t ld, int64_t cols, bool gated) {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
             if constexpr (KC) {
-                const int r = (j * NW + wave) * 8 + (lane >> 3);
-                voff[j] = (uint32_t)(r * (int)ld * 2 + piece(j, wave, lane) * 16);
+                const int r = row(j, wave, lane);
+                const int c = (lane & 7) ^ ((r & 3) | (((r >> SH) & 1) << 2));
+                kpiece = c * 8;
+                voff[j] = (uint32_t)((gated ? (r >> 6) * 32 + (r & 31) : r) * (int)ld * 2 + c * 16);
             } else {
                 const int at = (j * NW + wave) * 1024 + lane * 16;
                 const int k = at / (R * 2), p = (at % (R * 2)) / 16;
@@ -294,26 +312,11 @@ struct DnStream {
             }
         }
     }
-    // the 16-byte piece of its row that lane loads (k-rows)
-    __device__ __forceinline__ static int piece(int j, int wave, int lane) {
-        const int r = (j * NW + wave) * 8 + (lane >> 3);
-        return (lane & 7) ^ ((r & 3) | (((r >> SH) & 1) << 2));
+    // load j; past: OR-ed into the offset (DN_OOB: this lane's k is past K)
+    __device__ __forceinline__ void issue(int j, u32x4 r, uint32_t dst, int wave, uint32_t past) {
+        dn_load_lds(r, dst + (j * NW + wave) * 1024, KC ? voff[j] | past : voff[j]);
     }
-    // k-rows: base = the tile's first row at k0, kleft = K - k0 (> 0); rows
-    // left is in the buffer's size.  b2: second half of every 64 rows (gated)
-    __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t r, lds_u8 *dst, int wave, int lane, int kleft) {
-        if (KC && kleft < DN_BK) {
-#pragma unroll
-            for (int j = 0; j < NL; ++j) {
-                const uint32_t v = piece(j, wave, lane) * 8 < kleft ? voff[j] : DN_OOB;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst + (j * NW + wave) * 1024, 16, v, 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NL; ++j)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst + (j * NW + wave) * 1024, 16, voff[j], 0, 0, 0);
-        }
-    }
+    __device__ __forceinline__ uint32_t past(int kleft) const { return KC && kpiece >= kleft ? DN_OOB : 0u; }
 };
 
 // Row of the tile that row i of fragment j stands for: CG fragments share a
@@ -340,8 +343,67 @@ __device__ __forceinline__ void dn_tile(const DenseParams &P, int b, int &tm, in
     tm = grp * G + in - tn * rows;
 }
 
+struct DnTrue {
+    static constexpr bool value = true;
+};
+struct DnFalse {
+    static constexpr bool value = false;
+};
+
+// Where the next loads read: the current product's operands at the step's k.
+// An operand's range (bytes from its pointer) shrinks with it and is zero
+// after the last step, so loads past the end fetch nothing.
+template <bool AKC, bool BKC, bool GATED>
+struct DnCursor {
+    const uint16_t *a, *b, *b2;
+    int kleft;       // k left in this product, 0 after the last step
+    int na, nb;      // ranges of k-rows operands
+    int64_t sa, sb;  // elements from one step to the next
+    int seg;
+
+    __device__ __forceinline__ void open(const DenseParams &P, int i, int k0, int64_t m0, int64_t n0, int rows, int cols) {
+        const DenseSeg &g = P.seg[i];
+        seg = i;
+        kleft = g.K - k0;
+        a = AKC ? g.a + m0 * g.lda + k0 : g.a + k0 * g.lda + m0;
+        b = BKC ? g.b + n0 * g.ldb + k0 : g.b + k0 * g.ldb + n0;
+        if constexpr (GATED) b2 = g.b2 + n0 * g.ldb + k0;
+        sa = AKC ? DN_BK : DN_BK * g.lda;
+        sb = BKC ? DN_BK : DN_BK * g.ldb;
+        na = AKC ? (rows * (int)g.lda - k0) * 2 : 0;
+        nb = BKC ? (cols * (int)g.ldb - k0) * 2 : 0;
+    }
+    __device__ __forceinline__ void advance(const DenseParams &P, int64_t m0, int64_t n0, int rows, int cols) {
+        a += sa;
+        b += sb;
+        if constexpr (GATED) b2 += sb;
+        na -= DN_BK * 2;
+        nb -= DN_BK * 2;
+        kleft -= DN_BK;
+        if (kleft <= 0) {
+            if (seg + 1 < P.nseg)
+                open(P, seg + 1, 0, m0, n0, rows, cols);
+            else
+                kleft = 0;
+        }
+    }
+    // transposed: the rows left of this step, from the tile's first column on
+    __device__ __forceinline__ int range_a(const DenseParams &P, int64_t m0) const {
+        return kleft <= 0 ? 0 : AKC ? na : (min(DN_BK, kleft) * (int)P.seg[0].lda - (int)m0) * 2;
+    }
+    __device__ __forceinline__ int range_b(const DenseParams &P, int64_t n0) const {
+        return kleft <= 0 ? 0 : BKC ? nb : (min(DN_BK, kleft) * (int)P.seg[0].ldb - (int)n0) * 2;
+    }
+};
+
+// Main loop.  A step's 64 k are two halves of 32.  Fragments are double
+// buffered in registers: while the MFMAs of one half run, the other half's
+// fragments are read, so no MFMA waits for LDS.  In the middle of a step one
+// barrier says both that every wave has read the whole step (its buffer is
+// free: the loads of step s+2 go out) and that step s+1, loaded since the
+// middle of the step before, has landed.
 template <int BM, int BN, int WM, int WN, int FORM, int EPI>
-__global__ __launch_bounds__(WM *WN * 64, 2) void k_dense(DenseParams P) {
+__global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P) {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the stub alone: it drops stubs of templates that use the buffer builtins)
     constexpr int NW = WM * WN;
     constexpr bool AKC = FORM != DN_TN, BKC = FORM == DN_NT;
@@ -349,7 +411,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_dense(DenseParams P) {
     constexpr int MS = BM / WM / 16, NS = BN / WN / 16;  // 16 x 16 blocks per wave
     constexpr int CG = BKC ? (GATED ? 2 : 4) : 1;        // (transposed reads keep 16 consecutive columns)
     constexpr int SHB = CG == 4 ? 4 : CG == 2 ? 3 : 2;
-    static_assert(!GATED || NS == 4, "gate and up halves of 64 weight rows");
+    static_assert(!GATED || NS % 4 == 0, "gate and up halves of 64 weight rows");
     static_assert(NS % CG == 0, "whole runs");
     typedef DnStream<BM, AKC, NW, 2> SA;
     typedef DnStream<BN, BKC, NW, SHB> SB;
@@ -365,64 +427,53 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_dense(DenseParams P) {
     const int64_t m0 = (int64_t)tm * BM;
     constexpr int BNF = GATED ? BN / 2 : BN;  // output columns per tile
     const int64_t n0 = (int64_t)tn * BNF;
+    const int rows = (int)min((int64_t)BM, P.M - m0), cols = (int)min((int64_t)BNF, P.N - n0);
     const int s_end = min(P.steps, ((int)blockIdx.y + 1) * P.steps_per_split);
     int s = (int)blockIdx.y * P.steps_per_split;
 
     SA sa;
     SB sb;
-    // the product (of the sum) and k that the next loads take
-    int seg = 0, k0 = s * DN_BK;
-    while (seg + 1 < P.nseg && k0 >= (P.seg[seg].K + DN_BK - 1) / DN_BK * DN_BK) {
-        k0 -= (P.seg[seg].K + DN_BK - 1) / DN_BK * DN_BK;
-        ++seg;
-    }
-    sa.setup(wave, lane, P.seg[0].lda, P.M - m0);
-    // gated: the tile's 64-row groups hold 32 gate rows, then the same 32 up rows
-    if constexpr (GATED) {
-        static_assert(!GATED || SB::NL * NW * 8 == BN, "rows per load");
-#pragma unroll
-        for (int j = 0; j < SB::NL; ++j) {
-            const int r = (j * NW + wave) * 8 + (lane >> 3);
-            const int f = (r >> 6) * 32 + (r & 31);
-            sb.voff[j] = (uint32_t)(f * (int)P.seg[0].ldb * 2 + SB::piece(j, wave, lane) * 16);
-        }
-    } else {
-        sb.setup(wave, lane, P.seg[0].ldb, P.N - n0);
-    }
-
-    auto load = [&](int buf) {
-        const DenseSeg &g = P.seg[seg];
-        lds_u8 *da = lds + buf * STAGE, *db = da + SA::BYTES;
-        const int kleft = g.K - k0;
-        if constexpr (AKC)
-            sa.issue(dn_rsrc(g.a + m0 * g.lda + k0, ((int64_t)min((int64_t)BM, P.M - m0) * g.lda - k0) * 2), da, wave, lane,
-                     kleft);
-        else
-            sa.issue(dn_rsrc(g.a + k0 * g.lda + m0, ((int64_t)min(DN_BK, kleft) * g.lda - m0) * 2), da, wave, lane, kleft);
-        if constexpr (GATED) {
-            const int64_t bytes = ((int64_t)min((int64_t)BNF, P.N - n0) * g.ldb - k0) * 2;
-            const __amdgpu_buffer_rsrc_t rg = dn_rsrc(g.b + n0 * g.ldb + k0, bytes), ru = dn_rsrc(g.b2 + n0 * g.ldb + k0, bytes);
-#pragma unroll
-            for (int j = 0; j < SB::NL; ++j) {
-                uint32_t v = sb.voff[j];
-                if (kleft < DN_BK) v = SB::piece(j, wave, lane) * 8 < kleft ? v : DN_OOB;
-                const bool up = (((j * NW + wave) * 8) >> 5) & 1;
-                if (up)
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, db + (j * NW + wave) * 1024, 16, v, 0, 0, 0);
-                else
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rg, db + (j * NW + wave) * 1024, 16, v, 0, 0, 0);
-            }
-        } else if constexpr (BKC) {
-            sb.issue(dn_rsrc(g.b + n0 * g.ldb + k0, ((int64_t)min((int64_t)BN, P.N - n0) * g.ldb - k0) * 2), db, wave, lane,
-                     kleft);
-        } else {
-            sb.issue(dn_rsrc(g.b + k0 * g.ldb + n0, ((int64_t)min(DN_BK, kleft) * g.ldb - n0) * 2), db, wave, lane, kleft);
-        }
-        k0 += DN_BK;
-        if (k0 >= g.K) {
-            k0 = 0;
+    DnCursor<AKC, BKC, GATED> cur;
+    {
+        int seg = 0, k0 = s * DN_BK;
+        while (seg + 1 < P.nseg && k0 >= P.seg[seg].K) {  // (steps of a product: its K rounded up)
+            k0 -= (P.seg[seg].K + DN_BK - 1) / DN_BK * DN_BK;
             ++seg;
         }
+        cur.open(P, seg, k0, m0, n0, rows, cols);
+    }
+    sa.setup(wave, lane, P.seg[0].lda, rows, false);
+    sb.setup(wave, lane, P.seg[0].ldb, cols, GATED);
+    int left = s_end - s;  // steps not yet loaded
+
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+    // the next step's loads: load_begin, load_one(0 .. NLD - 1), load_end
+    constexpr int NLD = SA::NL + SB::NL;
+    u32x4 ra, rb, ru;
+    uint32_t pa, pb, da;
+    auto load_begin = [&](int buf) {
+        da = lds0 + buf * STAGE;
+        pa = sa.past(cur.kleft);
+        pb = sb.past(cur.kleft);
+        const int nb = left > 0 ? cur.range_b(P, n0) : 0;
+        ra = dn_rsrc(cur.a, left > 0 ? cur.range_a(P, m0) : 0);
+        rb = dn_rsrc(cur.b, nb);
+        if constexpr (GATED) ru = dn_rsrc(cur.b2, nb);
+    };
+    auto load_one = [&](int j) {
+        if (j < SA::NL) {
+            sa.issue(j, ra, da, wave, pa);
+        } else {
+            j -= SA::NL;
+            // (8 rows per load and wave: all of one matrix)
+            const bool up = GATED && ((((j * NW + wave) * 8) >> 5) & 1);
+            sb.issue(j, up ? ru : rb, da + SA::BYTES, wave, pb);
+        }
+    };
+    auto load_end = [&]() {
+        --left;
+        cur.advance(P, m0, n0, rows, cols);
     };
 
     float4v acc[MS][NS];
@@ -444,35 +495,67 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_dense(DenseParams P) {
         return *(lds_bf16x8 *)(base + ((at ^ (kk << 6)) + row * 128));
     };
     auto frag_tr = [&](lds_u8 *base, uint32_t at, int blk, int ld2, int kk) {
-        const uint32_t o = at + (((blk ^ tg)) << 5) + kk * 32 * ld2;
+        const uint32_t o = at + ((blk ^ tg) << 5) + kk * 32 * ld2;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(base + o));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(base + o + 4 * ld2));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
         return __builtin_bit_cast(bf16x8, s16x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w});
     };
-
-    if (s < s_end) load(0);
-    for (int buf = 0; s < s_end; ++s, buf ^= 1) {
-        wait_vm<0>();   // this wave's loads of step s have landed
-        lds_barrier();  // every wave's have, and every wave has read step s-1
-        if (s + 1 < s_end) load(buf ^ 1);
+    bf16x8 fa[2][MS], fb[2][NS];
+    // fragment q of a half: the weight side's first, then the activations'
+    auto read_one = [&](int set, int buf, int kk, int q) {
         lds_u8 *ba = lds + buf * STAGE, *bb = ba + SA::BYTES;
+        if (q < NS)
+            fb[set][q] = BKC ? frag_kc(bb, b_kc, dn_row<CG>(0, q), kk) : frag_tr(bb, b_tr, b_row / 16 + q, BN * 2, kk);
+        else
+            fa[set][q - NS] = AKC ? frag_kc(ba, a_kc, 16 * (q - NS), kk) : frag_tr(ba, a_tr, a_row / 16 + q - NS, BM * 2, kk);
+    };
+    constexpr int NF = NS + MS;
+    // one half: MS groups of NS MFMAs on `set`, among them the reads of the
+    // other half into the other set (done before the last group, so that the
+    // next half starts at once) and, with LD, the next loads; the order is
+    // fixed (the compiler's own gathers the reads in front of a full wait)
+    auto half = [&](auto ld, int set, int buf, int kk) {
+        constexpr bool LD = decltype(ld)::value;
+        constexpr int RG = MS > 1 ? MS - 1 : 1;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            bf16x8 fb[NS], fa[MS];
+        for (int i = 0; i < MS; ++i) {
+            if constexpr (LD) {
+#pragma unroll
+                for (int j = 0; j < NLD; ++j)
+                    if (j * MS / NLD == i) load_one(j);
+            }
 #pragma unroll
             for (int j = 0; j < NS; ++j)
-                fb[j] = BKC ? frag_kc(bb, b_kc, dn_row<CG>(0, j), kk) : frag_tr(bb, b_tr, b_row / 16 + j, BN * 2, kk);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < MS; ++i)
-                fa[i] = AKC ? frag_kc(ba, a_kc, 16 * i, kk) : frag_tr(ba, a_tr, a_row / 16 + i, BM * 2, kk);
-#pragma unroll
-            for (int i = 0; i < MS; ++i)
-#pragma unroll
-                for (int j = 0; j < NS; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+            for (int q = 0; q < NF; ++q)
+                if (q * RG / NF == i) read_one(set ^ 1, buf, kk, q);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        load_begin(b);
+#pragma unroll
+        for (int j = 0; j < NLD; ++j) load_one(j);
+        load_end();
     }
+    wait_vm<NLD>();
+    lds_barrier();
+#pragma unroll
+    for (int q = 0; q < NF; ++q) read_one(0, 0, 0, q);
+    for (int buf = 0; s < s_end; ++s, buf ^= 1) {
+        load_begin(buf);
+        half(DnFalse(), 0, buf, 1);
+        wait_vm<0>();
+        lds_barrier();
+        half(DnTrue(), 1, buf ^ 1, 0);
+        load_end();
+    }
+    wait_vm<0>();  // (the last loads: their LDS is released when the workgroup ends)
 
     // results: row m = 16 i + li, columns from 4 CG lg on
     constexpr int V = CG == 1 ? 4 : 8;
@@ -481,20 +564,23 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_dense(DenseParams P) {
         const int64_t m = m0 + a_row + 16 * i + li;
         if (m >= P.M) continue;
         if constexpr (GATED) {
-            const int n = (int)n0 + wn * 32 + 8 * lg;
-            if (n >= P.N) continue;
-            float g[8], u[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                g[k] = acc[i][k >> 2][k & 3];
-                u[k] = acc[i][2 + (k >> 2)][k & 3];
-            }
-            if (P.splits > 1) {
-                float *p = P.part + ((int64_t)blockIdx.y * P.M + m) * (2 * (int64_t)P.N) + n;
-                dn_store_f32<8>(p, g);
-                dn_store_f32<8>(p + P.N, u);
-            } else {
-                dn_epi_gated<8>(P.e, P.M, P.N, m, n, g, u);
+            for (int q = 0; q < NS / 4; ++q) {
+                const int n = (int)n0 + (b_row >> 1) + 32 * q + 8 * lg;
+                if (n >= P.N) continue;
+                float g[8], u[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    g[k] = acc[i][4 * q + (k >> 2)][k & 3];
+                    u[k] = acc[i][4 * q + 2 + (k >> 2)][k & 3];
+                }
+                if (P.splits > 1) {
+                    float *p = P.part + ((int64_t)blockIdx.y * P.M + m) * (2 * (int64_t)P.N) + n;
+                    dn_store_f32<8>(p, g);
+                    dn_store_f32<8>(p + P.N, u);
+                } else {
+                    dn_epi_gated<8>(P.e, P.M, P.N, m, n, g, u);
+                }
             }
         } else {
 #pragma unroll
