@@ -350,58 +350,56 @@ struct DnFalse {
     static constexpr bool value = false;
 };
 
-// Where the next loads read: the current product's operands at the step's k.
-// An operand's range (bytes from its pointer) shrinks with it and is zero
+// Where an operand's next loads read: the current product's matrix at the
+// step's k.  The range (bytes from the pointer) shrinks with it and is zero
 // after the last step, so loads past the end fetch nothing.
-template <bool AKC, bool BKC, bool GATED>
+template <bool KC, bool B>
 struct DnCursor {
-    const uint16_t *a, *b, *b2;
-    int kleft;       // k left in this product, 0 after the last step
-    int na, nb;      // ranges of k-rows operands
-    int64_t sa, sb;  // elements from one step to the next
-    int seg;
+    const uint16_t *p, *p2;  // p2: the up projection
+    int64_t step;            // elements from one step to the next
+    int kleft;               // k left in this product
+    int bytes;               // k-rows: the range
+    int ld, seg, left;       // left: steps not yet loaded
 
-    __device__ __forceinline__ void open(const DenseParams &P, int i, int k0, int64_t m0, int64_t n0, int rows, int cols) {
+    // first: the tile's first row or column; n: its rows
+    __device__ __forceinline__ void open(const DenseParams &P, int i, int k0, int64_t first, int n) {
         const DenseSeg &g = P.seg[i];
+        const int64_t l = B ? g.ldb : g.lda;
+        const int64_t at = KC ? first * l + k0 : k0 * l + first;
         seg = i;
+        ld = (int)l;
         kleft = g.K - k0;
-        a = AKC ? g.a + m0 * g.lda + k0 : g.a + k0 * g.lda + m0;
-        b = BKC ? g.b + n0 * g.ldb + k0 : g.b + k0 * g.ldb + n0;
-        if constexpr (GATED) b2 = g.b2 + n0 * g.ldb + k0;
-        sa = AKC ? DN_BK : DN_BK * g.lda;
-        sb = BKC ? DN_BK : DN_BK * g.ldb;
-        na = AKC ? (rows * (int)g.lda - k0) * 2 : 0;
-        nb = BKC ? (cols * (int)g.ldb - k0) * 2 : 0;
+        p = (B ? g.b : g.a) + at;
+        p2 = B ? g.b2 + at : nullptr;
+        step = KC ? DN_BK : DN_BK * l;
+        bytes = (n * ld - k0) * 2;
     }
-    __device__ __forceinline__ void advance(const DenseParams &P, int64_t m0, int64_t n0, int rows, int cols) {
-        a += sa;
-        b += sb;
-        if constexpr (GATED) b2 += sb;
-        na -= DN_BK * 2;
-        nb -= DN_BK * 2;
+    __device__ __forceinline__ void advance(const DenseParams &P, int64_t first, int n) {
+        p += step;
+        p2 += step;
+        bytes -= DN_BK * 2;
         kleft -= DN_BK;
-        if (kleft <= 0) {
-            if (seg + 1 < P.nseg)
-                open(P, seg + 1, 0, m0, n0, rows, cols);
-            else
-                kleft = 0;
-        }
+        --left;
+        if (kleft <= 0 && left > 0) open(P, seg + 1, 0, first, n);
     }
     // transposed: the rows left of this step, from the tile's first column on
-    __device__ __forceinline__ int range_a(const DenseParams &P, int64_t m0) const {
-        return kleft <= 0 ? 0 : AKC ? na : (min(DN_BK, kleft) * (int)P.seg[0].lda - (int)m0) * 2;
-    }
-    __device__ __forceinline__ int range_b(const DenseParams &P, int64_t n0) const {
-        return kleft <= 0 ? 0 : BKC ? nb : (min(DN_BK, kleft) * (int)P.seg[0].ldb - (int)n0) * 2;
+    __device__ __forceinline__ int range(int64_t first) const {
+        return left <= 0 ? 0 : KC ? bytes : (min(DN_BK, kleft) * ld - (int)first) * 2;
     }
 };
 
 // Main loop.  A step's 64 k are two halves of 32.  Fragments are double
 // buffered in registers: while the MFMAs of one half run, the other half's
-// fragments are read, so no MFMA waits for LDS.  In the middle of a step one
-// barrier says both that every wave has read the whole step (its buffer is
-// free: the loads of step s+2 go out) and that step s+1, loaded since the
-// middle of the step before, has landed.
+// fragments are read, so no MFMA waits for LDS.  LDS holds a ring of five
+// operand slices (one operand, one step), loaded in the order B0 A0 B1 A1 ...:
+// the first half of step s loads B of s+2 into the slice left over, the second
+// half A of s+2 into one of the two that step s has been read from.  One
+// barrier, in the middle of a step, says both that every wave has read step s
+// and that step s+1 has landed.  Loads go out through the whole step: the
+// path into LDS moves 64 bytes a cycle, half the step's MFMA time for a
+// 256 x 256 tile, and loads bunched in one half of it hold up the MFMAs
+// behind them (measured, 8192 x 4096 x 4096: all within a quarter step 222 us,
+// half a step 196 us).
 template <int BM, int BN, int WM, int WN, int FORM, int EPI>
 __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P) {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the stub alone: it drops stubs of templates that use the buffer builtins)
@@ -415,8 +413,9 @@ __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P
     static_assert(NS % CG == 0, "whole runs");
     typedef DnStream<BM, AKC, NW, 2> SA;
     typedef DnStream<BN, BKC, NW, SHB> SB;
-    constexpr int STAGE = SA::BYTES + SB::BYTES;
-    __shared__ __align__(1024) uint8_t smem[2 * STAGE];
+    static_assert(SA::BYTES == SB::BYTES, "slices of one size");
+    constexpr int SLICE = SA::BYTES;
+    __shared__ __align__(1024) uint8_t smem[5 * SLICE];
     lds_u8 *const lds = (lds_u8 *)smem;
 
     const int lane = threadIdx.x & 63;
@@ -433,48 +432,43 @@ __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P
 
     SA sa;
     SB sb;
-    DnCursor<AKC, BKC, GATED> cur;
+    DnCursor<AKC, false> ca;
+    DnCursor<BKC, true> cb;
     {
         int seg = 0, k0 = s * DN_BK;
         while (seg + 1 < P.nseg && k0 >= P.seg[seg].K) {  // (steps of a product: its K rounded up)
             k0 -= (P.seg[seg].K + DN_BK - 1) / DN_BK * DN_BK;
             ++seg;
         }
-        cur.open(P, seg, k0, m0, n0, rows, cols);
+        ca.open(P, seg, k0, m0, rows);
+        cb.open(P, seg, k0, n0, cols);
+        ca.left = cb.left = s_end - s;
     }
     sa.setup(wave, lane, P.seg[0].lda, rows, false);
     sb.setup(wave, lane, P.seg[0].ldb, cols, GATED);
-    int left = s_end - s;  // steps not yet loaded
-
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-    // the next step's loads: load_begin, load_one(0 .. NLD - 1), load_end
-    constexpr int NLD = SA::NL + SB::NL;
+    // an operand's next loads: *_begin(slice), *_one(0 .. NL - 1), then the cursor's advance
     u32x4 ra, rb, ru;
-    uint32_t pa, pb, da;
-    auto load_begin = [&](int buf) {
-        da = lds0 + buf * STAGE;
-        pa = sa.past(cur.kleft);
-        pb = sb.past(cur.kleft);
-        const int nb = left > 0 ? cur.range_b(P, n0) : 0;
-        ra = dn_rsrc(cur.a, left > 0 ? cur.range_a(P, m0) : 0);
-        rb = dn_rsrc(cur.b, nb);
-        if constexpr (GATED) ru = dn_rsrc(cur.b2, nb);
+    uint32_t pa, pb, da, db;
+    auto a_begin = [&](int slice) {
+        da = lds0 + slice * SLICE;
+        pa = sa.past(ca.kleft);
+        ra = dn_rsrc(ca.p, ca.range(m0));
     };
-    auto load_one = [&](int j) {
-        if (j < SA::NL) {
-            sa.issue(j, ra, da, wave, pa);
-        } else {
-            j -= SA::NL;
-            // (8 rows per load and wave: all of one matrix)
-            const bool up = GATED && ((((j * NW + wave) * 8) >> 5) & 1);
-            sb.issue(j, up ? ru : rb, da + SA::BYTES, wave, pb);
-        }
+    auto a_one = [&](int j) { sa.issue(j, ra, da, wave, pa); };
+    auto b_begin = [&](int slice) {
+        db = lds0 + slice * SLICE;
+        pb = sb.past(cb.kleft);
+        rb = dn_rsrc(cb.p, cb.range(n0));
+        if constexpr (GATED) ru = dn_rsrc(cb.p2, cb.range(n0));
     };
-    auto load_end = [&]() {
-        --left;
-        cur.advance(P, m0, n0, rows, cols);
+    auto b_one = [&](int j) {
+        // (8 rows per load and wave: all of one matrix)
+        const bool up = GATED && ((((j * NW + wave) * 8) >> 5) & 1);
+        sb.issue(j, up ? ru : rb, db, wave, pb);
     };
+    auto wrap = [](int n) { return n >= 5 ? n - 5 : n; };
 
     float4v acc[MS][NS];
 #pragma unroll
@@ -503,57 +497,68 @@ __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P
     };
     bf16x8 fa[2][MS], fb[2][NS];
     // fragment q of a half: the weight side's first, then the activations'
-    auto read_one = [&](int set, int buf, int kk, int q) {
-        lds_u8 *ba = lds + buf * STAGE, *bb = ba + SA::BYTES;
+    auto read_one = [&](int set, lds_u8 *ba, lds_u8 *bb, int kk, int q) {
         if (q < NS)
             fb[set][q] = BKC ? frag_kc(bb, b_kc, dn_row<CG>(0, q), kk) : frag_tr(bb, b_tr, b_row / 16 + q, BN * 2, kk);
         else
             fa[set][q - NS] = AKC ? frag_kc(ba, a_kc, 16 * (q - NS), kk) : frag_tr(ba, a_tr, a_row / 16 + q - NS, BM * 2, kk);
     };
     constexpr int NF = NS + MS;
-    // one half: MS groups of NS MFMAs on `set`, among them the reads of the
+    // one half: MS groups of NS MFMAs on `set`, between them the reads of the
     // other half into the other set (done before the last group, so that the
-    // next half starts at once) and, with LD, the next loads; the order is
+    // next half starts at once) and one operand's next loads; the order is
     // fixed (the compiler's own gathers the reads in front of a full wait)
-    auto half = [&](auto ld, int set, int buf, int kk) {
-        constexpr bool LD = decltype(ld)::value;
+    auto half = [&](auto load_a, int set, int slice_a, int slice_b, int kk) {
+        constexpr bool LA = decltype(load_a)::value;
+        constexpr int NL = LA ? SA::NL : SB::NL;
         constexpr int RG = MS > 1 ? MS - 1 : 1;
+        lds_u8 *ba = lds + slice_a * SLICE, *bb = lds + slice_b * SLICE;
 #pragma unroll
         for (int i = 0; i < MS; ++i) {
-            if constexpr (LD) {
 #pragma unroll
-                for (int j = 0; j < NLD; ++j)
-                    if (j * MS / NLD == i) load_one(j);
-            }
+            for (int j = 0; j < NL; ++j)
+                if (j * MS / NL == i) {
+                    if (LA)
+                        a_one(j);
+                    else
+                        b_one(j);
+                }
 #pragma unroll
             for (int j = 0; j < NS; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int q = 0; q < NF; ++q)
-                if (q * RG / NF == i) read_one(set ^ 1, buf, kk, q);
+                if (q * RG / NF == i) read_one(set ^ 1, ba, bb, kk, q);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
 
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        load_begin(b);
+    for (int t = 0; t < 2; ++t) {
+        b_begin(2 * t);
 #pragma unroll
-        for (int j = 0; j < NLD; ++j) load_one(j);
-        load_end();
+        for (int j = 0; j < SB::NL; ++j) b_one(j);
+        cb.advance(P, n0, cols);
+        a_begin(2 * t + 1);
+#pragma unroll
+        for (int j = 0; j < SA::NL; ++j) a_one(j);
+        ca.advance(P, m0, rows);
     }
-    wait_vm<NLD>();
+    wait_vm<SA::NL + SB::NL>();
     lds_barrier();
 #pragma unroll
-    for (int q = 0; q < NF; ++q) read_one(0, 0, 0, q);
-    for (int buf = 0; s < s_end; ++s, buf ^= 1) {
-        load_begin(buf);
-        half(DnFalse(), 0, buf, 1);
-        wait_vm<0>();
+    for (int q = 0; q < NF; ++q) read_one(0, lds + SLICE, lds, 0, q);
+    // slice of step s's B; A's is the next, then B and A of s+1, B of s+2
+    for (int sl = 0; s < s_end; ++s, sl = wrap(sl + 2)) {
+        b_begin(wrap(sl + 4));
+        half(DnFalse(), 0, wrap(sl + 1), sl, 1);
+        cb.advance(P, n0, cols);
+        a_begin(sl);
+        wait_vm<SB::NL>();
         lds_barrier();
-        half(DnTrue(), 1, buf ^ 1, 0);
-        load_end();
+        half(DnTrue(), 1, wrap(sl + 3), wrap(sl + 2), 0);
+        ca.advance(P, m0, rows);
     }
     wait_vm<0>();  // (the last loads: their LDS is released when the workgroup ends)
 
