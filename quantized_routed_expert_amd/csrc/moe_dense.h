@@ -278,6 +278,13 @@ __device__ __forceinline__ void dn_epi(const DenseParams &P, int64_t m, int n, f
 // ---------------------------------------------------------------------------
 // Streaming one operand's slices into LDS
 // ---------------------------------------------------------------------------
+// g(k) of a transposed slice of R columns (a 64-column row is 128 bytes: its
+// four blocks and the row's parity make the eight places)
+template <int R>
+__device__ __forceinline__ int dn_swap(int k) {
+    return R >= 128 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
+}
+
 // KC: R rows of 64 k.  SH: the bit of the row that joins its two low bits in
 // s(r) (2: fragments of 16 consecutive rows; 3, 4: rows in runs of 2 or 4
 // fragments, see dn_row).  Otherwise: 64 k of R columns.
@@ -285,7 +292,7 @@ template <int R, bool KC, int NW, int SH>
 struct DnStream {
     static constexpr int NL = R * 128 / 1024 / NW;  // loads per wave and step
     static constexpr int BYTES = R * 128;
-    static_assert(R * 128 % (1024 * NW) == 0, "whole wave loads");
+    static_assert(NL * NW * 1024 == BYTES, "whole wave loads");
     static_assert(!KC || SH == 2 || (8 * NW) % (2 << SH) == 0, "one piece for all of a lane's rows");
     uint32_t voff[NL];
     int kpiece;  // k-rows: the first k of the 16-byte piece that this lane loads of each of its rows
@@ -293,21 +300,20 @@ struct DnStream {
     // row of the tile whose piece (k-rows) the lane loads with load j
     __device__ __forceinline__ static int row(int j, int wave, int lane) { return (j * NW + wave) * 8 + (lane >> 3); }
     // ld in elements; cols: columns left from the tile's first (transposed).
-    // gated: the tile's 64-row groups hold 32 rows of one matrix, then the
-    // same 32 rows of another
-    __device__ __forceinline__ void setup(int wave, int lane, int64_t ld, int64_t cols, bool gated) {
+    // pair != 0 (gated): the tile's rows are groups of `pair` rows of one
+    // matrix and the same rows of another
+    __device__ __forceinline__ void setup(int wave, int lane, int64_t ld, int64_t cols, int pair) {
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
             if constexpr (KC) {
                 const int r = row(j, wave, lane);
                 const int c = (lane & 7) ^ ((r & 3) | (((r >> SH) & 1) << 2));
                 kpiece = c * 8;
-                voff[j] = (uint32_t)((gated ? (r >> 6) * 32 + (r & 31) : r) * (int)ld * 2 + c * 16);
+                voff[j] = (uint32_t)((pair ? r / (2 * pair) * pair + r % pair : r) * (int)ld * 2 + c * 16);
             } else {
                 const int at = (j * NW + wave) * 1024 + lane * 16;
                 const int k = at / (R * 2), p = (at % (R * 2)) / 16;
-                const int g = (k & 3) | (((k >> 3) & 1) << 2);
-                const int c = p ^ (g << 1);
+                const int c = p ^ (dn_swap<R>(k) << 1);
                 voff[j] = c * 8 < cols ? (uint32_t)(k * (int)ld * 2 + c * 16) : DN_OOB;
             }
         }
@@ -390,85 +396,94 @@ struct DnCursor {
 
 // Main loop.  A step's 64 k are two halves of 32.  Fragments are double
 // buffered in registers: while the MFMAs of one half run, the other half's
-// fragments are read, so no MFMA waits for LDS.  LDS holds a ring of five
-// operand slices (one operand, one step), loaded in the order B0 A0 B1 A1 ...:
-// the first half of step s loads B of s+2 into the slice left over, the second
-// half A of s+2 into one of the two that step s has been read from.  One
-// barrier, in the middle of a step, says both that every wave has read step s
-// and that step s+1 has landed.  Loads go out through the whole step: the
-// path into LDS moves 64 bytes a cycle, half the step's MFMA time for a
-// 256 x 256 tile, and loads bunched in one half of it hold up the MFMAs
-// behind them (measured, 8192 x 4096 x 4096: all within a quarter step 222 us,
-// half a step 196 us).
-template <int BM, int BN, int WM, int WN, int FORM, int EPI>
-__global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P) {
+// fragments are read, so no MFMA waits for LDS.  LDS holds three slices of B
+// and two of A (a slice: one operand, one step).  The first half of step s
+// loads B of s+2 into its third slice, the second half A of s+2 into the one
+// that A of s has just been read from.  One barrier, in the middle of a step,
+// says both that every wave has read step s and that step s+1 has landed.
+// Loads go out through the whole step: the path into LDS moves 64 bytes a
+// cycle, half the step's MFMA time for a 256 x 256 tile, and loads bunched in
+// one half of it hold up the MFMAs behind them (measured, 8192 x 4096 x 4096:
+// all within a quarter step 222 us, half a step 196 us).
+//
+// KG > 1: the workgroup's waves are KG groups, each with its own slices and
+// its own part of the tile's steps; their sums are added in LDS, in order, at
+// the end.  Small tiles spend their time waiting for loads; the groups keep
+// KG times as many in flight and take 1 / KG of the steps.
+template <int BM, int BN, int WM, int WN, int KG, int FORM, int EPI>
+__global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(DenseParams P) {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the stub alone: it drops stubs of templates that use the buffer builtins)
-    constexpr int NW = WM * WN;
+    constexpr int NW = WM * WN;  // waves per group
     constexpr bool AKC = FORM != DN_TN, BKC = FORM == DN_NT;
     constexpr bool GATED = EPI == DN_EPI_GATED;
     constexpr int MS = BM / WM / 16, NS = BN / WN / 16;  // 16 x 16 blocks per wave
-    constexpr int CG = BKC ? (GATED ? 2 : 4) : 1;        // (transposed reads keep 16 consecutive columns)
+    // (transposed reads keep 16 consecutive columns)
+    constexpr int CG = !BKC ? 1 : GATED ? (NS >= 4 ? 2 : 1) : (NS >= 4 ? 4 : NS);
     constexpr int SHB = CG == 4 ? 4 : CG == 2 ? 3 : 2;
-    static_assert(!GATED || NS % 4 == 0, "gate and up halves of 64 weight rows");
-    static_assert(NS % CG == 0, "whole runs");
+    constexpr int PAIR = GATED ? 16 * CG : 0;  // gate rows, then up rows, of a run of fragments
+    static_assert(NS % (GATED ? 2 * CG : CG) == 0, "whole runs");
     typedef DnStream<BM, AKC, NW, 2> SA;
     typedef DnStream<BN, BKC, NW, SHB> SB;
-    static_assert(SA::BYTES == SB::BYTES, "slices of one size");
-    constexpr int SLICE = SA::BYTES;
-    __shared__ __align__(1024) uint8_t smem[5 * SLICE];
-    lds_u8 *const lds = (lds_u8 *)smem;
+    constexpr int RING = 2 * SA::BYTES + 3 * SB::BYTES;
+    static_assert(KG == 1 || (KG - 1) * BM * BN * 4 <= RING * KG, "the groups' sums fit the slices");
+    __shared__ __align__(1024) uint8_t smem[RING * KG];
+    lds_u8 *const lds_all = (lds_u8 *)smem;
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int grp = KG > 1 ? wave_all / NW : 0;
+    const int wave = KG > 1 ? wave_all % NW : wave_all;
     const int wm = wave / WN, wn = wave % WN;
+    lds_u8 *const lds = lds_all + grp * RING;
     int tm, tn;
     dn_tile(P, blockIdx.x, tm, tn);
     const int64_t m0 = (int64_t)tm * BM;
     constexpr int BNF = GATED ? BN / 2 : BN;  // output columns per tile
     const int64_t n0 = (int64_t)tn * BNF;
     const int rows = (int)min((int64_t)BM, P.M - m0), cols = (int)min((int64_t)BNF, P.N - n0);
-    const int s_end = min(P.steps, ((int)blockIdx.y + 1) * P.steps_per_split);
-    int s = (int)blockIdx.y * P.steps_per_split;
+    // this group's steps (a group past the end multiplies zeros)
+    const int s_wg = (int)blockIdx.y * P.steps_per_split, e_wg = min(P.steps, s_wg + P.steps_per_split);
+    const int nstep = KG > 1 ? (e_wg - s_wg + KG - 1) / KG : e_wg - s_wg;
+    const int s0 = s_wg + grp * nstep;
 
     SA sa;
     SB sb;
     DnCursor<AKC, false> ca;
     DnCursor<BKC, true> cb;
     {
-        int seg = 0, k0 = s * DN_BK;
+        int seg = 0, k0 = s0 * DN_BK;
         while (seg + 1 < P.nseg && k0 >= P.seg[seg].K) {  // (steps of a product: its K rounded up)
             k0 -= (P.seg[seg].K + DN_BK - 1) / DN_BK * DN_BK;
             ++seg;
         }
         ca.open(P, seg, k0, m0, rows);
         cb.open(P, seg, k0, n0, cols);
-        ca.left = cb.left = s_end - s;
+        ca.left = cb.left = min(nstep, e_wg - s0);
     }
-    sa.setup(wave, lane, P.seg[0].lda, rows, false);
-    sb.setup(wave, lane, P.seg[0].ldb, cols, GATED);
+    sa.setup(wave, lane, P.seg[0].lda, rows, 0);
+    sb.setup(wave, lane, P.seg[0].ldb, cols, PAIR);
     const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
     // an operand's next loads: *_begin(slice), *_one(0 .. NL - 1), then the cursor's advance
     u32x4 ra, rb, ru;
     uint32_t pa, pb, da, db;
     auto a_begin = [&](int slice) {
-        da = lds0 + slice * SLICE;
+        da = lds0 + slice * SA::BYTES;
         pa = sa.past(ca.kleft);
         ra = dn_rsrc(ca.p, ca.range(m0));
     };
     auto a_one = [&](int j) { sa.issue(j, ra, da, wave, pa); };
     auto b_begin = [&](int slice) {
-        db = lds0 + slice * SLICE;
+        db = lds0 + 2 * SA::BYTES + slice * SB::BYTES;
         pb = sb.past(cb.kleft);
         rb = dn_rsrc(cb.p, cb.range(n0));
         if constexpr (GATED) ru = dn_rsrc(cb.p2, cb.range(n0));
     };
     auto b_one = [&](int j) {
         // (8 rows per load and wave: all of one matrix)
-        const bool up = GATED && ((((j * NW + wave) * 8) >> 5) & 1);
+        const bool up = GATED && (((j * NW + wave) * 8 / (PAIR ? PAIR : 1)) & 1);
         sb.issue(j, up ? ru : rb, db, wave, pb);
     };
-    auto wrap = [](int n) { return n >= 5 ? n - 5 : n; };
 
     float4v acc[MS][NS];
 #pragma unroll
@@ -481,15 +496,15 @@ __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P
     const int a_row = wm * (BM / WM), b_row = wn * (BN / WN);
     const uint32_t a_kc = (uint32_t)((a_row + li) * 128 + ((lg ^ (li & 7)) << 4));
     const uint32_t b_kc = (uint32_t)((b_row + dn_row<CG>(li, 0)) * 128 + ((lg ^ (li & 7)) << 4));
-    const int tg = (li >> 2) | ((lg & 1) << 2);  // g(k) of the k rows this lane addresses
-    const int tk = 8 * lg + (li >> 2);
+    const int tk = 8 * lg + (li >> 2);  // the k row this lane addresses (and tk + 4, + 32: the same g)
+    const int ga = dn_swap<BM>(tk), gb = dn_swap<BN>(tk);
     const uint32_t a_tr = (uint32_t)(tk * BM * 2 + (li & 3) * 8), b_tr = (uint32_t)(tk * BN * 2 + (li & 3) * 8);
 
     auto frag_kc = [&](lds_u8 *base, uint32_t at, int row, int kk) {
         return *(lds_bf16x8 *)(base + ((at ^ (kk << 6)) + row * 128));
     };
     auto frag_tr = [&](lds_u8 *base, uint32_t at, int blk, int ld2, int kk) {
-        const uint32_t o = at + ((blk ^ tg) << 5) + kk * 32 * ld2;
+        const uint32_t o = at + (blk << 5) + kk * 32 * ld2;
         const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(base + o));
         const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(base + o + 4 * ld2));
         typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -499,20 +514,19 @@ __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P
     // fragment q of a half: the weight side's first, then the activations'
     auto read_one = [&](int set, lds_u8 *ba, lds_u8 *bb, int kk, int q) {
         if (q < NS)
-            fb[set][q] = BKC ? frag_kc(bb, b_kc, dn_row<CG>(0, q), kk) : frag_tr(bb, b_tr, b_row / 16 + q, BN * 2, kk);
+            fb[set][q] = BKC ? frag_kc(bb, b_kc, dn_row<CG>(0, q), kk) : frag_tr(bb, b_tr, (b_row / 16 + q) ^ gb, BN * 2, kk);
         else
-            fa[set][q - NS] = AKC ? frag_kc(ba, a_kc, 16 * (q - NS), kk) : frag_tr(ba, a_tr, a_row / 16 + q - NS, BM * 2, kk);
+            fa[set][q - NS] = AKC ? frag_kc(ba, a_kc, 16 * (q - NS), kk) : frag_tr(ba, a_tr, (a_row / 16 + q - NS) ^ ga, BM * 2, kk);
     };
     constexpr int NF = NS + MS;
     // one half: MS groups of NS MFMAs on `set`, between them the reads of the
     // other half into the other set (done before the last group, so that the
     // next half starts at once) and one operand's next loads; the order is
     // fixed (the compiler's own gathers the reads in front of a full wait)
-    auto half = [&](auto load_a, int set, int slice_a, int slice_b, int kk) {
+    auto half = [&](auto load_a, int set, lds_u8 *ba, lds_u8 *bb, int kk) {
         constexpr bool LA = decltype(load_a)::value;
         constexpr int NL = LA ? SA::NL : SB::NL;
         constexpr int RG = MS > 1 ? MS - 1 : 1;
-        lds_u8 *ba = lds + slice_a * SLICE, *bb = lds + slice_b * SLICE;
 #pragma unroll
         for (int i = 0; i < MS; ++i) {
 #pragma unroll
@@ -536,31 +550,55 @@ __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P
 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        b_begin(2 * t);
+        b_begin(t);
 #pragma unroll
         for (int j = 0; j < SB::NL; ++j) b_one(j);
         cb.advance(P, n0, cols);
-        a_begin(2 * t + 1);
+        a_begin(t);
 #pragma unroll
         for (int j = 0; j < SA::NL; ++j) a_one(j);
         ca.advance(P, m0, rows);
     }
     wait_vm<SA::NL + SB::NL>();
     lds_barrier();
+    lds_u8 *const lds_b = lds + 2 * SA::BYTES;
 #pragma unroll
-    for (int q = 0; q < NF; ++q) read_one(0, lds + SLICE, lds, 0, q);
-    // slice of step s's B; A's is the next, then B and A of s+1, B of s+2
-    for (int sl = 0; s < s_end; ++s, sl = wrap(sl + 2)) {
-        b_begin(wrap(sl + 4));
-        half(DnFalse(), 0, wrap(sl + 1), sl, 1);
+    for (int q = 0; q < NF; ++q) read_one(0, lds, lds_b, 0, q);
+    // slices of step s: A's sl_a, B's sl_b
+    for (int s = 0, sl_a = 0, sl_b = 0; s < nstep; ++s) {
+        const int nb = sl_b == 2 ? 0 : sl_b + 1;
+        b_begin(nb == 2 ? 0 : nb + 1);
+        half(DnFalse(), 0, lds + sl_a * SA::BYTES, lds_b + sl_b * SB::BYTES, 1);
         cb.advance(P, n0, cols);
-        a_begin(sl);
+        a_begin(sl_a);
         wait_vm<SB::NL>();
         lds_barrier();
-        half(DnTrue(), 1, wrap(sl + 3), wrap(sl + 2), 0);
+        sl_a ^= 1;
+        sl_b = nb;
+        half(DnTrue(), 1, lds + sl_a * SA::BYTES, lds_b + sl_b * SB::BYTES, 0);
         ca.advance(P, m0, rows);
     }
     wait_vm<0>();  // (the last loads: their LDS is released when the workgroup ends)
+
+    if constexpr (KG > 1) {  // the groups' sums, in order, by the first group
+        __syncthreads();
+        float4v *const sums = (float4v *)smem;
+        constexpr int PER = MS * NS * 64;  // of one wave
+        if (grp > 0) {
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+#pragma unroll
+                for (int j = 0; j < NS; ++j) sums[((grp - 1) * NW + wave) * PER + (i * NS + j) * 64 + lane] = acc[i][j];
+        }
+        __syncthreads();
+        if (grp > 0) return;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+            for (int i = 0; i < MS; ++i)
+#pragma unroll
+                for (int j = 0; j < NS; ++j) acc[i][j] += sums[(g * NW + wave) * PER + (i * NS + j) * 64 + lane];
+    }
 
     // results: row m = 16 i + li, columns from 4 CG lg on
     constexpr int V = CG == 1 ? 4 : 8;
@@ -570,21 +608,21 @@ __global__ __launch_bounds__(WM *WN * 64, WM *WN / 4) void k_dense(DenseParams P
         if (m >= P.M) continue;
         if constexpr (GATED) {
 #pragma unroll
-            for (int q = 0; q < NS / 4; ++q) {
-                const int n = (int)n0 + (b_row >> 1) + 32 * q + 8 * lg;
+            for (int q = 0; q < NS / (2 * CG); ++q) {
+                const int n = (int)n0 + (b_row >> 1) + 16 * CG * q + 4 * CG * lg;
                 if (n >= P.N) continue;
-                float g[8], u[8];
+                float g[V], u[V];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    g[k] = acc[i][4 * q + (k >> 2)][k & 3];
-                    u[k] = acc[i][4 * q + 2 + (k >> 2)][k & 3];
+                for (int k = 0; k < V; ++k) {
+                    g[k] = acc[i][2 * CG * q + (k >> 2)][k & 3];
+                    u[k] = acc[i][2 * CG * q + CG + (k >> 2)][k & 3];
                 }
                 if (P.splits > 1) {
                     float *p = P.part + ((int64_t)blockIdx.y * P.M + m) * (2 * (int64_t)P.N) + n;
-                    dn_store_f32<8>(p, g);
-                    dn_store_f32<8>(p + P.N, u);
+                    dn_store_f32<V>(p, g);
+                    dn_store_f32<V>(p + P.N, u);
                 } else {
-                    dn_epi_gated<8>(P.e, P.M, P.N, m, n, g, u);
+                    dn_epi_gated<V>(P.e, P.M, P.N, m, n, g, u);
                 }
             }
         } else {
@@ -642,10 +680,21 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseParams P) {
 template <int FORM, int EPI>
 hipError_t dense_launch_t(const DenseParams &P, int tile, hipStream_t st) {
     const dim3 grid((unsigned)(P.tiles_m * P.tiles_n), (unsigned)P.splits);
-    if (tile == DN_TILE_256)
-        hipLaunchKernelGGL((k_dense<256, 256, 2, 4, FORM, EPI>), grid, dim3(512), 0, st, P);
-    else
-        hipLaunchKernelGGL((k_dense<128, 128, 2, 2, FORM, EPI>), grid, dim3(256), 0, st, P);
+    switch (tile) {
+        case DN_TILE_256x256:
+            hipLaunchKernelGGL((k_dense<256, 256, 2, 4, 1, FORM, EPI>), grid, dim3(512), 0, st, P);
+            break;
+        case DN_TILE_256x128:
+            hipLaunchKernelGGL((k_dense<256, 128, 4, 2, 1, FORM, EPI>), grid, dim3(512), 0, st, P);
+            break;
+        case DN_TILE_128x128:
+            hipLaunchKernelGGL((k_dense<128, 128, 2, 2, 2, FORM, EPI>), grid, dim3(512), 0, st, P);
+            break;
+        case DN_TILE_64x64:
+            hipLaunchKernelGGL((k_dense<64, 64, 2, 2, 4, FORM, EPI>), grid, dim3(1024), 0, st, P);
+            break;
+        default: return hipErrorInvalidValue;
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || P.splits == 1) return e;
     const int64_t work = (int64_t)P.M * (P.N / 8);

@@ -53,21 +53,41 @@ bool misaligned(const void *p) { return ((uintptr_t)p & 15) != 0; }
 struct Plan {
     int tile, tiles_m, tiles_n, splits, per;
 };
+// Tile and split: the least estimated time over the tiles and split counts.
+// A launch takes rounds of one tile per CU; a tile takes a fixed time and one
+// per step (of its longest group), a split adds the parts' traffic and the
+// joining launch.
+struct TileCost {
+    int bm, bn, groups;
+    double fixed, step;  // us
+};
+constexpr TileCost TILES[DN_TILES] = {{256, 256, 1, 9.0, 1.36}, {256, 128, 1, 6.0, 0.75}, {128, 128, 2, 5.0, 0.9}, {64, 64, 4, 4.0, 0.6}};
+#ifdef DN_FORCE
+int g_force_tile = -1, g_force_split = 1;
+#endif
 // C of M x N columns of the weight side (gated: 2F) over `steps` 64-k steps
 Plan make_plan(int64_t M, int64_t N, int64_t steps) {
-    Plan p;
-    const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256);
-    p.tile = t256 >= 192 ? DN_TILE_256 : DN_TILE_128;
-    const int bt = p.tile == DN_TILE_256 ? 256 : 128;
-    p.tiles_m = (int)ceil_div(M, bt);
-    p.tiles_n = (int)ceil_div(N, bt);
-    const int64_t tiles = max64((int64_t)p.tiles_m * p.tiles_n, 1);  // (M = 0: nothing is launched)
-    int64_t s = p.tile == DN_TILE_256 ? 1 : DN_SPLIT_TILES / tiles;
-    if (s > steps / 4) s = steps / 4;
-    if (s < 1) s = 1;
-    p.per = (int)ceil_div(steps > 0 ? steps : 1, s);
-    p.splits = (int)ceil_div(steps > 0 ? steps : 1, p.per);
-    return p;
+    Plan best = {-1, 0, 0, 1, 1};
+    double best_t = 1e30;
+    for (int t = 0; t < DN_TILES; ++t) {
+        const TileCost &c = TILES[t];
+        const int64_t tm = ceil_div(M, c.bm), tn = ceil_div(N, c.bn), tiles = max64(tm * tn, 1);  // (M = 0: nothing is launched)
+        for (int64_t s = 1; s <= 16; s *= 2) {
+#ifdef DN_FORCE
+            if (g_force_tile >= 0 && (t != g_force_tile || s != g_force_split)) continue;
+#endif
+            if (s > 1 && (tiles * s * c.bm * c.bn > (int64_t)DN_SPLIT_TILES * 128 * 128 || steps < 4 * s * c.groups)) break;
+            const int64_t per = ceil_div(max64(steps, 1), s);
+            const double rounds = (double)ceil_div(tiles * s, 256);
+            double us = rounds * (c.fixed + c.step * (double)ceil_div(per, c.groups));
+            if (s > 1) us += 6.0 + (double)(s * M * N) * 8.0 / 4.0e6;
+            if (us < best_t) {
+                best_t = us;
+                best = Plan{t, (int)tm, (int)tn, (int)ceil_div(max64(steps, 1), per), (int)per};
+            }
+        }
+    }
+    return best;
 }
 int64_t ksteps(int64_t K) { return ceil_div(K, DN_BK); }
 
@@ -163,6 +183,9 @@ int x_segments(DenseParams &P, const void *x, bool x_f32, int64_t T, int64_t K, 
 }  // namespace
 
 extern "C" {
+#ifdef DN_FORCE
+void dn_force(int tile, int split) { g_force_tile = tile; g_force_split = split; }
+#endif
 
 int64_t moe_linear_workspace_bytes(int32_t T, int32_t in, int32_t out) {
     int rc = check_rows(T);
