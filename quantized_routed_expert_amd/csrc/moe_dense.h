@@ -11,7 +11,7 @@
 //
 // The weight side (N) feeds the MFMA's row operand, the activation side (M)
 // its column operand: D's rows are n, four consecutive per lane, so a lane
-// holds runs along the output's contiguous axis.
+// holds runs along the output's contiguous axis (joined to eight, dn_join).
 //
 // An operand whose rows run along k is read as 16-byte fragments (8 k); one
 // whose rows run along m or n ("transposed") with ds_read_b64_tr_b16, which
@@ -170,6 +170,14 @@ __device__ __forceinline__ float dn_act1(int act, float v, float &d) {
             return v;
     }
 }
+// ACT of the epilogues: an activation, or DN_ACT_ANY: e.act, looked at at run
+// time (with the switch in each of a tile's unrolled units the code outgrows
+// the instruction cache: 256 x 256 tiles took 5 us longer)
+constexpr int DN_ACT_ANY = -1;
+template <int ACT>
+__device__ __forceinline__ int dn_act_of(const DenseEpi &e) {
+    return ACT == DN_ACT_ANY ? e.act : ACT;
+}
 template <int V>
 __device__ __forceinline__ void dn_act(int act, float (&v)[V]) {
     float d;
@@ -181,7 +189,7 @@ __device__ __forceinline__ void dn_act(int act, float (&v)[V]) {
 // Epilogues: V consecutive columns from n on of row m
 // ---------------------------------------------------------------------------
 // z = v + bias (kept in bf16 if asked); y = act(z) + residual
-template <int V>
+template <int V, int ACT>
 __device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
     const int64_t at = m * N + n;
     if (e.bias) {
@@ -191,7 +199,7 @@ __device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t 
         for (int i = 0; i < V; ++i) v[i] += b[i];
     }
     if (e.z) dn_store_bf<V>(e.z + at, v);
-    if (e.act) dn_act<V>(e.act, v);
+    if (dn_act_of<ACT>(e) != DN_ACT_NONE) dn_act<V>(dn_act_of<ACT>(e), v);
     if (e.res) {
         float r[V];
         if (e.res_f32)
@@ -209,14 +217,14 @@ __device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t 
 // h = act(g) u.  h enters the down product in bf16; with h_terms = 3 (an fp32
 // y) as three exact bf16 terms, so that y is as good as its type.  g and u
 // kept for the backward pass are rounded to bf16 (the type that pass reads).
-template <int V>
+template <int V, int ACT>
 __device__ __forceinline__ void dn_epi_gated(const DenseEpi &e, int64_t M, int N, int64_t m, int n, float (&g)[V],
                                              float (&u)[V]) {
     if (e.gu) {
         dn_store_bf<V>(e.gu + m * (2 * (int64_t)N) + n, g);
         dn_store_bf<V>(e.gu + m * (2 * (int64_t)N) + N + n, u);
     }
-    dn_act<V>(e.act, g);
+    dn_act<V>(dn_act_of<ACT>(e), g);
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] *= u[i];
     if (e.h_terms == 3)
@@ -226,7 +234,7 @@ __device__ __forceinline__ void dn_epi_gated(const DenseEpi &e, int64_t M, int N
 }
 // v = dh: h = act(g) u, dg = dh u act'(g), du = dh act(g), each rounded once
 // to bf16, the type their products take
-template <int V>
+template <int V, int ACT>
 __device__ __forceinline__ void dn_epi_dgated(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
     float g[V], u[V], h[V], dg[V], du[V];
     const int64_t at = m * (2 * (int64_t)N) + n;
@@ -235,7 +243,7 @@ __device__ __forceinline__ void dn_epi_dgated(const DenseEpi &e, int N, int64_t 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float d;
-        const float a = dn_act1<true>(e.act, g[i], d);
+        const float a = dn_act1<true>(dn_act_of<ACT>(e), g[i], d);
         h[i] = a * u[i];
         dg[i] = v[i] * u[i] * d;
         du[i] = v[i] * a;
@@ -268,10 +276,10 @@ __device__ __forceinline__ void dn_epi_grad(const DenseEpi &e, int N, int64_t m,
     else
         dn_store_bf<V>((uint16_t *)y + at, v);
 }
-template <int EPI, int V>
+template <int EPI, int V, int ACT>
 __device__ __forceinline__ void dn_epi(const DenseParams &P, int64_t m, int n, float (&v)[V]) {
-    if constexpr (EPI == DN_EPI_LINEAR) dn_epi_linear<V>(P.e, P.N, m, n, v);
-    if constexpr (EPI == DN_EPI_DGATED) dn_epi_dgated<V>(P.e, P.N, m, n, v);
+    if constexpr (EPI == DN_EPI_LINEAR) dn_epi_linear<V, ACT>(P.e, P.N, m, n, v);
+    if constexpr (EPI == DN_EPI_DGATED) dn_epi_dgated<V, ACT>(P.e, P.N, m, n, v);
     if constexpr (EPI == DN_EPI_GRAD) dn_epi_grad<V>(P.e, P.N, m, n, v);
 }
 
@@ -285,15 +293,12 @@ __device__ __forceinline__ int dn_swap(int k) {
     return R >= 128 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
 }
 
-// KC: R rows of 64 k.  SH: the bit of the row that joins its two low bits in
-// s(r) (2: fragments of 16 consecutive rows; 3, 4: rows in runs of 2 or 4
-// fragments, see dn_row).  Otherwise: 64 k of R columns.
-template <int R, bool KC, int NW, int SH>
+// KC: R rows of 64 k, s(r) = r % 8.  Otherwise: 64 k of R columns.
+template <int R, bool KC, int NW>
 struct DnStream {
     static constexpr int NL = R * 128 / 1024 / NW;  // loads per wave and step
     static constexpr int BYTES = R * 128;
     static_assert(NL * NW * 1024 == BYTES, "whole wave loads");
-    static_assert(!KC || SH == 2 || (8 * NW) % (2 << SH) == 0, "one piece for all of a lane's rows");
     uint32_t voff[NL];
     int kpiece;  // k-rows: the first k of the 16-byte piece that this lane loads of each of its rows
 
@@ -307,7 +312,7 @@ struct DnStream {
         for (int j = 0; j < NL; ++j) {
             if constexpr (KC) {
                 const int r = row(j, wave, lane);
-                const int c = (lane & 7) ^ ((r & 3) | (((r >> SH) & 1) << 2));
+                const int c = (lane & 7) ^ (r & 7);
                 kpiece = c * 8;
                 voff[j] = (uint32_t)((pair ? r / (2 * pair) * pair + r % pair : r) * (int)ld * 2 + c * 16);
             } else {
@@ -325,12 +330,23 @@ struct DnStream {
     __device__ __forceinline__ uint32_t past(int kleft) const { return KC && kpiece >= kleft ? DN_OOB : 0u; }
 };
 
-// Row of the tile that row i of fragment j stands for: CG fragments share a
-// run of 16 CG rows, four consecutive ones each in turn, so that a lane's CG
-// results are 4 CG consecutive rows.
-template <int CG>
-__device__ __forceinline__ constexpr int dn_row(int i, int j) {
-    return (i >> 2) * 4 * CG + (j % CG) * 4 + (i & 3) + (j / CG) * 16 * CG;
+// Two blocks' results (lane group lg: four columns from 4 lg on of each) ->
+// eight consecutive columns from dn_joined(lg) on of the pair, so that a bf16
+// store is 16 bytes and a row's four lanes write 64 in one piece.  (Stores of
+// 16 bytes in every 32 took 8 us of a 256 x 256 tile; the path takes one
+// 64-byte piece of a line at a time.)
+__device__ __forceinline__ int dn_joined(int lg) { return 16 * (lg & 1) + 8 * (lg >> 1); }
+__device__ __forceinline__ void dn_join(float4v a, float4v b, float (&v)[8]) {
+    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        // lane groups (0 1 2 3) of a and b -> a0 b0 a2 b2 and a1 b1 a3 b3
+        const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, av[k]), __builtin_bit_cast(uint32_t, bv[k]),
+                                                        false, false);
+        const uint32_t lo = r[0], hi = r[1];  // (copied out: a bit cast of a component reads the first)
+        v[k] = __builtin_bit_cast(float, lo);
+        v[4 + k] = __builtin_bit_cast(float, hi);
+    }
 }
 
 // Workgroup -> tile: workgroups go round robin over the 8 XCDs, so each XCD
@@ -410,22 +426,19 @@ struct DnCursor {
 // its own part of the tile's steps; their sums are added in LDS, in order, at
 // the end.  Small tiles spend their time waiting for loads; the groups keep
 // KG times as many in flight and take 1 / KG of the steps.
-template <int BM, int BN, int WM, int WN, int KG, int FORM, int EPI>
+template <int BM, int BN, int WM, int WN, int KG, int FORM, int EPI, int ACT>
 __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(DenseParams P) {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the stub alone: it drops stubs of templates that use the buffer builtins)
     constexpr int NW = WM * WN;  // waves per group
     constexpr bool AKC = FORM != DN_TN, BKC = FORM == DN_NT;
     constexpr bool GATED = EPI == DN_EPI_GATED;
     constexpr int MS = BM / WM / 16, NS = BN / WN / 16;  // 16 x 16 blocks per wave
-    // (transposed reads keep 16 consecutive columns)
-    constexpr int CG = !BKC ? 1 : GATED ? (NS >= 4 ? 2 : 1) : (NS >= 4 ? 4 : NS);
-    constexpr int SHB = CG == 4 ? 4 : CG == 2 ? 3 : 2;
-    constexpr int PAIR = GATED ? 16 * CG : 0;  // gate rows, then up rows, of a run of fragments
-    static_assert(NS % (GATED ? 2 * CG : CG) == 0, "whole runs");
-    typedef DnStream<BM, AKC, NW, 2> SA;
-    typedef DnStream<BN, BKC, NW, SHB> SB;
+    static_assert(NS % 2 == 0, "pairs of blocks");
+    constexpr int PAIR = GATED ? 16 : 0;  // blocks of 16 gate rows and the same up rows in turn
+    typedef DnStream<BM, AKC, NW> SA;
+    typedef DnStream<BN, BKC, NW> SB;
     constexpr int RING = 2 * SA::BYTES + 3 * SB::BYTES;
-    static_assert(KG == 1 || (KG - 1) * BM * BN * 4 <= RING * KG, "the groups' sums fit the slices");
+    static_assert(KG == 1 || BM * BN * 4 <= RING, "the groups' sums fit the slices");
     __shared__ __align__(1024) uint8_t smem[RING * KG];
     lds_u8 *const lds_all = (lds_u8 *)smem;
 
@@ -495,7 +508,7 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
     const int li = lane & 15, lg = lane >> 4;
     const int a_row = wm * (BM / WM), b_row = wn * (BN / WN);
     const uint32_t a_kc = (uint32_t)((a_row + li) * 128 + ((lg ^ (li & 7)) << 4));
-    const uint32_t b_kc = (uint32_t)((b_row + dn_row<CG>(li, 0)) * 128 + ((lg ^ (li & 7)) << 4));
+    const uint32_t b_kc = (uint32_t)((b_row + li) * 128 + ((lg ^ (li & 7)) << 4));
     const int tk = 8 * lg + (li >> 2);  // the k row this lane addresses (and tk + 4, + 32: the same g)
     const int ga = dn_swap<BM>(tk), gb = dn_swap<BN>(tk);
     const uint32_t a_tr = (uint32_t)(tk * BM * 2 + (li & 3) * 8), b_tr = (uint32_t)(tk * BN * 2 + (li & 3) * 8);
@@ -514,7 +527,7 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
     // fragment q of a half: the weight side's first, then the activations'
     auto read_one = [&](int set, lds_u8 *ba, lds_u8 *bb, int kk, int q) {
         if (q < NS)
-            fb[set][q] = BKC ? frag_kc(bb, b_kc, dn_row<CG>(0, q), kk) : frag_tr(bb, b_tr, (b_row / 16 + q) ^ gb, BN * 2, kk);
+            fb[set][q] = BKC ? frag_kc(bb, b_kc, 16 * q, kk) : frag_tr(bb, b_tr, (b_row / 16 + q) ^ gb, BN * 2, kk);
         else
             fa[set][q - NS] = AKC ? frag_kc(ba, a_kc, 16 * (q - NS), kk) : frag_tr(ba, a_tr, (a_row / 16 + q - NS) ^ ga, BM * 2, kk);
     };
@@ -580,64 +593,88 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
     }
     wait_vm<0>();  // (the last loads: their LDS is released when the workgroup ends)
 
-    if constexpr (KG > 1) {  // the groups' sums, in order, by the first group
+    // Results in units: (row block i, pair of column blocks).  With groups,
+    // unit u belongs to group u % KG, which adds the others' sums from LDS.
+    // A unit's two column blocks are j, j + 1; gated: the gate blocks j, j + 2
+    // (with the up blocks after them), or one gate block where a wave has one.
+    constexpr int JP = GATED && NS == 2 ? 1 : 2, UJ = NS / (GATED ? 2 * JP : JP);
+    typedef float4v LdsSums[KG][NW][MS * NS][64];
+    if constexpr (KG > 1) {
         __syncthreads();
-        float4v *const sums = (float4v *)smem;
-        constexpr int PER = MS * NS * 64;  // of one wave
-        if (grp > 0) {
+        LdsSums &sums = *(LdsSums *)smem;
 #pragma unroll
-            for (int i = 0; i < MS; ++i)
+        for (int i = 0; i < MS; ++i)
 #pragma unroll
-                for (int j = 0; j < NS; ++j) sums[((grp - 1) * NW + wave) * PER + (i * NS + j) * 64 + lane] = acc[i][j];
-        }
+            for (int j = 0; j < NS; ++j) sums[grp][wave][i * NS + j][lane] = acc[i][j];
         __syncthreads();
-        if (grp > 0) return;
-#pragma unroll
-        for (int g = 0; g < KG - 1; ++g)
-#pragma unroll
-            for (int i = 0; i < MS; ++i)
-#pragma unroll
-                for (int j = 0; j < NS; ++j) acc[i][j] += sums[(g * NW + wave) * PER + (i * NS + j) * 64 + lane];
     }
-
-    // results: row m = 16 i + li, columns from 4 CG lg on
-    constexpr int V = CG == 1 ? 4 : 8;
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
         const int64_t m = m0 + a_row + 16 * i + li;
-        if (m >= P.M) continue;
-        if constexpr (GATED) {
 #pragma unroll
-            for (int q = 0; q < NS / (2 * CG); ++q) {
-                const int n = (int)n0 + (b_row >> 1) + 16 * CG * q + 4 * CG * lg;
-                if (n >= P.N) continue;
-                float g[V], u[V];
+        for (int uj = 0; uj < UJ; ++uj) {
+            if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
+            // the unit's sums, block by block
+            auto block = [&](int j) {
+                float4v v = acc[i][j];
+                if constexpr (KG > 1) {
+                    LdsSums &sums = *(LdsSums *)smem;
+                    v = sums[0][wave][i * NS + j][lane];
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    g[k] = acc[i][2 * CG * q + (k >> 2)][k & 3];
-                    u[k] = acc[i][2 * CG * q + CG + (k >> 2)][k & 3];
+                    for (int g = 1; g < KG; ++g) v += sums[g][wave][i * NS + j][lane];
+                }
+                return v;
+            };
+            if constexpr (GATED) {
+                const int j0 = uj * 2 * JP;
+                const int nb = (int)n0 + (b_row >> 1) + 16 * JP * uj;  // first column of the unit
+                float4v g[JP], u[JP];
+#pragma unroll
+                for (int p = 0; p < JP; ++p) {
+                    g[p] = block(j0 + 2 * p);
+                    u[p] = block(j0 + 2 * p + 1);
                 }
                 if (P.splits > 1) {
-                    float *p = P.part + ((int64_t)blockIdx.y * P.M + m) * (2 * (int64_t)P.N) + n;
-                    dn_store_f32<V>(p, g);
-                    dn_store_f32<V>(p + P.N, u);
+                    float *const part = P.part + ((int64_t)blockIdx.y * P.M + m) * (2 * (int64_t)P.N);
+#pragma unroll
+                    for (int p = 0; p < JP; ++p) {
+                        const int n = nb + 16 * p + 4 * lg;
+                        if (m < P.M && n < P.N) {
+                            *(float4v *)(part + n) = g[p];
+                            *(float4v *)(part + P.N + n) = u[p];
+                        }
+                    }
+                } else if constexpr (JP == 2) {
+                    float gv[8], uv[8];
+                    dn_join(g[0], g[1], gv);
+                    dn_join(u[0], u[1], uv);
+                    const int n = nb + dn_joined(lg);
+                    if (m < P.M && n < P.N) dn_epi_gated<8, ACT>(P.e, P.M, P.N, m, n, gv, uv);
                 } else {
-                    dn_epi_gated<V>(P.e, P.M, P.N, m, n, g, u);
+                    float gv[4] = {g[0].x, g[0].y, g[0].z, g[0].w}, uv[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+                    const int n = nb + 4 * lg;
+                    if (m < P.M && n < P.N) dn_epi_gated<4, ACT>(P.e, P.M, P.N, m, n, gv, uv);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < NS * 4 / V; ++j) {
-                const int jj = j * (V / 4);
-                const int n = (int)n0 + b_row + dn_row<CG>(4 * lg, jj);
-                if (n >= P.N) continue;
-                float v[V];
-#pragma unroll
-                for (int k = 0; k < V; ++k) v[k] = acc[i][jj + (k >> 2)][k & 3];
-                if (P.splits > 1)
-                    dn_store_f32<V>(P.part + ((int64_t)blockIdx.y * P.M + m) * P.N + n, v);
-                else
-                    dn_epi<EPI, V>(P, m, n, v);
+            } else {
+                const int nb = (int)n0 + b_row + 32 * uj;
+                const float4v v0 = block(2 * uj), v1 = block(2 * uj + 1);
+                if (P.splits > 1) {
+                    float *const part = P.part + ((int64_t)blockIdx.y * P.M + m) * P.N;
+                    const int n = nb + 4 * lg;
+                    if (m < P.M && n < P.N) *(float4v *)(part + n) = v0;
+                    if (m < P.M && n + 16 < P.N) *(float4v *)(part + n + 16) = v1;
+                } else if ((EPI == DN_EPI_LINEAR || EPI == DN_EPI_GRAD) && P.e.y_f32) {
+                    // fp32 results: four columns are 16 bytes, a row's four lanes 64
+                    const int n = nb + 4 * lg;
+                    float a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
+                    if (m < P.M && n < P.N) dn_epi<EPI, 4, ACT>(P, m, n, a);
+                    if (m < P.M && n + 16 < P.N) dn_epi<EPI, 4, ACT>(P, m, n + 16, b);
+                } else {
+                    float v[8];
+                    dn_join(v0, v1, v);
+                    const int n = nb + dn_joined(lg);
+                    if (m < P.M && n < P.N) dn_epi<EPI, 8, ACT>(P, m, n, v);
+                }
             }
         }
     }
@@ -670,32 +707,44 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseParams P) {
             }
         }
         if constexpr (GATED)
-            dn_epi_gated<8>(P.e, P.M, P.N, m, n, v, u);
+            dn_epi_gated<8, DN_ACT_ANY>(P.e, P.M, P.N, m, n, v, u);
         else
-            dn_epi<EPI, 8>(P, m, n, v);
+            dn_epi<EPI, 8, DN_ACT_ANY>(P, m, n, v);
     }
 }
 
 // One product of the given form and epilogue, and its join when it is split.
-template <int FORM, int EPI>
-hipError_t dense_launch_t(const DenseParams &P, int tile, hipStream_t st) {
+template <int FORM, int EPI, int ACT>
+hipError_t dense_tile_t(const DenseParams &P, int tile, hipStream_t st) {
     const dim3 grid((unsigned)(P.tiles_m * P.tiles_n), (unsigned)P.splits);
     switch (tile) {
         case DN_TILE_256x256:
-            hipLaunchKernelGGL((k_dense<256, 256, 2, 4, 1, FORM, EPI>), grid, dim3(512), 0, st, P);
+            hipLaunchKernelGGL((k_dense<256, 256, 2, 4, 1, FORM, EPI, ACT>), grid, dim3(512), 0, st, P);
             break;
         case DN_TILE_256x128:
-            hipLaunchKernelGGL((k_dense<256, 128, 4, 2, 1, FORM, EPI>), grid, dim3(512), 0, st, P);
+            hipLaunchKernelGGL((k_dense<256, 128, 4, 2, 1, FORM, EPI, ACT>), grid, dim3(512), 0, st, P);
             break;
         case DN_TILE_128x128:
-            hipLaunchKernelGGL((k_dense<128, 128, 2, 2, 2, FORM, EPI>), grid, dim3(512), 0, st, P);
+            hipLaunchKernelGGL((k_dense<128, 128, 2, 2, 2, FORM, EPI, ACT>), grid, dim3(512), 0, st, P);
             break;
         case DN_TILE_64x64:
-            hipLaunchKernelGGL((k_dense<64, 64, 2, 2, 4, FORM, EPI>), grid, dim3(1024), 0, st, P);
+            hipLaunchKernelGGL((k_dense<64, 64, 2, 2, 4, FORM, EPI, ACT>), grid, dim3(1024), 0, st, P);
             break;
         default: return hipErrorInvalidValue;
     }
-    hipError_t e = hipGetLastError();
+    return hipGetLastError();
+}
+template <int FORM, int EPI>
+hipError_t dense_launch_t(const DenseParams &P, int tile, hipStream_t st) {
+    hipError_t e;
+    constexpr bool A = EPI != DN_EPI_GRAD && !(FORM == DN_NN && EPI == DN_EPI_LINEAR);  // with an activation
+    switch (A && P.splits == 1 ? P.e.act : DN_ACT_NONE) {
+        case DN_ACT_SILU: e = dense_tile_t<FORM, EPI, A ? DN_ACT_SILU : 0>(P, tile, st); break;
+        case DN_ACT_GELU: e = dense_tile_t<FORM, EPI, A ? DN_ACT_GELU : 0>(P, tile, st); break;
+        case DN_ACT_GELU_TANH: e = dense_tile_t<FORM, EPI, A ? DN_ACT_GELU_TANH : 0>(P, tile, st); break;
+        case DN_ACT_RELU: e = dense_tile_t<FORM, EPI, A ? DN_ACT_RELU : 0>(P, tile, st); break;
+        default: e = dense_tile_t<FORM, EPI, DN_ACT_NONE>(P, tile, st); break;
+    }
     if (e != hipSuccess || P.splits == 1) return e;
     const int64_t work = (int64_t)P.M * (P.N / 8);
     const int64_t blocks = (work + 255) / 256;
