@@ -227,7 +227,9 @@ __device__ __forceinline__ void dn_epi_gated(const DenseEpi &e, int64_t M, int N
     dn_act<V>(dn_act_of<ACT>(e), g);
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] *= u[i];
-    if (e.h_terms == 3)
+    if (e.h_terms == 0)
+        dn_store_f32<V>((float *)e.h + m * N + n, g);
+    else if (e.h_terms == 3)
         dn_store_split3<V>(e.h + m * N + n, (size_t)M * N, g);
     else
         dn_store_bf<V>(e.h + m * N + n, g);

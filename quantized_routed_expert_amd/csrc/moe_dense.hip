@@ -18,6 +18,8 @@ hipError_t dense_gated_launch(const DenseParams &P, int tile, hipStream_t st);
 hipError_t dense_dgated_launch(const DenseParams &P, int tile, hipStream_t st);
 hipError_t dense_dx_launch(const DenseParams &P, int tile, hipStream_t st);
 hipError_t dense_dw_launch(const DenseParams &P, int tile, hipStream_t st);
+hipError_t dense_rows_linear_launch(const DenseRowsParams &P, hipStream_t st);
+hipError_t dense_rows_gated_launch(const DenseRowsParams &P, hipStream_t st);
 }  // namespace moe
 
 using namespace moe;
@@ -213,6 +215,19 @@ int moe_linear(const void *x, int32_t x_dtype, int32_t T, int32_t in, const void
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     int cus;
     if ((rc = device_cus(cus))) return rc;
+    DenseEpi e;
+    memset(&e, 0, sizeof(e));
+    e.bias = (const uint16_t *)bias;
+    e.res = residual;
+    e.res_f32 = r_dtype == MOE_DTYPE_F32;
+    e.y = y;
+    e.y_f32 = y_dtype == MOE_DTYPE_F32;
+    e.z = (uint16_t *)z;
+    e.act = act;
+    if (T <= DN_ROWS_MAX) {
+        const DenseRowsParams R{x, (const uint16_t *)w, nullptr, e, T, out, in, xf};
+        return launch_err(dense_rows_linear_launch(R, S(stream)));
+    }
     DenseParams P;
     memset(&P, 0, sizeof(P));
     if ((rc = x_segments(P, x, xf, T, in, (uint16_t *)at(ws, L.x3), S(stream)))) return rc;
@@ -221,13 +236,7 @@ int moe_linear(const void *x, int32_t x_dtype, int32_t T, int32_t in, const void
         P.seg[i].ldb = in;
     }
     set_plan(P, L.fwd, T, out, (int)(ksteps(in) * P.nseg), (float *)at(ws, L.part));
-    P.e.bias = (const uint16_t *)bias;
-    P.e.res = residual;
-    P.e.res_f32 = r_dtype == MOE_DTYPE_F32;
-    P.e.y = y;
-    P.e.y_f32 = y_dtype == MOE_DTYPE_F32;
-    P.e.z = (uint16_t *)z;
-    P.e.act = act;
+    P.e = e;
     return launch_err(dense_linear_launch(P, L.fwd.tile, S(stream)));
 }
 
@@ -325,6 +334,24 @@ int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn
     if ((rc = device_cus(cus))) return rc;
     const hipStream_t st = S(stream);
     uint16_t *h = (uint16_t *)at(ws, L.h);
+    DenseEpi eg, ed;  // gate and up; down
+    memset(&eg, 0, sizeof(eg));
+    memset(&ed, 0, sizeof(ed));
+    eg.act = w->act;
+    eg.h = h;
+    eg.h_terms = yf ? 3 : 1;
+    eg.gu = (uint16_t *)gu;
+    ed.res = residual;
+    ed.res_f32 = r_dtype == MOE_DTYPE_F32;
+    ed.y = y;
+    ed.y_f32 = yf;
+    if (T <= DN_ROWS_MAX) {
+        if (yf) eg.h_terms = 0;  // (fp32, split where it is read)
+        const DenseRowsParams G{x, (const uint16_t *)w->gate, (const uint16_t *)w->up, eg, T, F, H, xf};
+        if (dense_rows_gated_launch(G, st) != hipSuccess) return MOE_ERR_LAUNCH;
+        const DenseRowsParams D{h, (const uint16_t *)w->down, nullptr, ed, T, H, F, yf};
+        return launch_err(dense_rows_linear_launch(D, st));
+    }
     DenseParams P;
     memset(&P, 0, sizeof(P));
     if ((rc = x_segments(P, x, xf, T, H, (uint16_t *)at(ws, L.x3), st))) return rc;
@@ -334,10 +361,7 @@ int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn
         P.seg[i].ldb = H;
     }
     set_plan(P, L.gu, T, F, (int)(ksteps(H) * P.nseg), (float *)at(ws, L.part));
-    P.e.act = w->act;
-    P.e.h = h;
-    P.e.h_terms = yf ? 3 : 1;
-    P.e.gu = (uint16_t *)gu;
+    P.e = eg;
     if (dense_gated_launch(P, L.gu.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
     DenseParams D;
     memset(&D, 0, sizeof(D));
@@ -345,10 +369,7 @@ int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn
     for (int i = 0; i < D.nseg; ++i)
         D.seg[i] = DenseSeg{h + (int64_t)i * T * F, (const uint16_t *)w->down, nullptr, F, F, F};
     set_plan(D, L.down, T, H, (int)(ksteps(F) * D.nseg), (float *)at(ws, L.part));
-    D.e.res = residual;
-    D.e.res_f32 = r_dtype == MOE_DTYPE_F32;
-    D.e.y = y;
-    D.e.y_f32 = yf;
+    D.e = ed;
     return launch_err(dense_linear_launch(D, L.down.tile, st));
 }
 

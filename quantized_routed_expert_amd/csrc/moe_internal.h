@@ -301,7 +301,8 @@ struct DenseEpi {
     const uint16_t *gu_in;  // gated backward: the kept gate and up
     uint16_t *dgu;          // gated backward: their gradients [M][2N]
     int m_split;
-    int act, y_f32, res_f32, h_terms, accumulate;
+    int act, y_f32, res_f32, accumulate;
+    int h_terms;  // 1 or 3 bf16 terms; 0: h is one plane of fp32
 };
 
 struct DenseParams {
@@ -312,6 +313,16 @@ struct DenseParams {
     int M, N;         // output rows and columns (gated: N = F)
     int tiles_m, tiles_n;
     int splits, steps_per_split;
+};
+
+// Few rows (a decode window): C = A B^T by streaming B once, k split over
+// waves; A in bf16 or fp32.
+constexpr int DN_ROWS_MAX = 16;
+struct DenseRowsParams {
+    const void *a;             // [M][K]
+    const uint16_t *b, *b2;    // [N][K] (b2: up)
+    DenseEpi e;
+    int M, N, K, a_f32;
 };
 
 // product forms: C = A B^T (rows of both run along k), C = A B (B's rows run

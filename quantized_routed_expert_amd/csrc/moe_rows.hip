@@ -1,0 +1,151 @@
+// moe_rows.hip -- C = A B^T for a decode window (M <= 16 rows): the weights
+// are read once, straight into the registers that the MFMA takes, and nothing
+// else costs: bound by the weights' bytes and, below some 10 MB, by the launch
+// and one round trip to memory.
+//
+// One workgroup takes 16 weight rows (8 with HALVES = 2), its 8 waves a part
+// of K each.  v_mfma_f32_16x16x32_bf16: the weight rows are the row operand,
+// the activation rows the column operand.  With HALVES = 2 (M <= 8) operand
+// rows 8..15 are the same 8 weight rows at another part of K and columns
+// 8..15 the same activations there; the two diagonal blocks of the result are
+// the two parts' sums, so no lane loads a byte twice and twice as many
+// workgroups share a small matrix.  Parts are summed in LDS in their order.
+//
+// A bf16 activation is an operand as it is; an fp32 one enters as its three
+// exact bf16 terms (three MFMAs on one weight fragment).
+#include "moe_dense.h"
+
+namespace moe {
+
+constexpr int RW_WAVES = 8;
+constexpr int RW_U = 8;  // 32-k loads in flight per wave (two such sets)
+
+template <int XF32>
+struct RwSet {
+    u32x4 w[RW_U], x[RW_U][XF32 ? 2 : 1];
+};
+
+template <int EPI, int XF32, int HALVES>
+__global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P) {
+    constexpr bool GATED = EPI == DN_EPI_GATED;
+    constexpr int R = 16 / HALVES;             // weight rows per workgroup
+    constexpr int RN = GATED ? R / 2 : R;      // output columns per workgroup
+    constexpr int PARTS = RW_WAVES * HALVES;
+    __shared__ __align__(16) float s_part[PARTS][16 / HALVES][R + 4];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lg = lane >> 4;
+    const int half = HALVES == 2 ? li >> 3 : 0, r = HALVES == 2 ? li & 7 : li;
+    const int n0 = blockIdx.x * RN;
+    // rows past the end read a valid row and are never stored
+    const int n = min(n0 + (GATED ? r % RN : r), P.N - 1), t = min(r, P.M - 1);
+    const uint16_t *wr = (GATED && r >= RN ? P.b2 : P.b) + (int64_t)n * P.K;
+    // this lane's part of K: 32-k pieces from k0 on
+    const int pieces = (P.K + 31) / 32, per = (pieces + PARTS - 1) / PARTS;
+    const int k0 = (wave * HALVES + half) * per * 32 + 8 * lg;
+
+    auto load = [&](RwSet<XF32> &s, int i0) {
+#pragma unroll
+        for (int i = 0; i < RW_U; ++i) {
+            const int k = k0 + (i0 + i) * 32;
+            // (a piece past the part or past K is zero in both operands)
+            const bool in = i0 + i < per && k < P.K;
+            const u32x4 z = {0u, 0u, 0u, 0u};
+            s.w[i] = z;
+            s.x[i][0] = z;
+            if (XF32) s.x[i][XF32] = z;
+            if (in) {
+                s.w[i] = *(const u32x4 *)(wr + k);
+                if constexpr (XF32) {
+                    const float *xr = (const float *)P.a + (int64_t)t * P.K + k;
+                    s.x[i][0] = *(const u32x4 *)xr;
+                    s.x[i][1] = *(const u32x4 *)(xr + 4);
+                } else {
+                    s.x[i][0] = *(const u32x4 *)((const uint16_t *)P.a + (int64_t)t * P.K + k);
+                }
+            }
+        }
+    };
+    float4v acc = {0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const RwSet<XF32> &s) {
+#pragma unroll
+        for (int i = 0; i < RW_U; ++i) {
+            const bf16x8 w = __builtin_bit_cast(bf16x8, s.w[i]);
+            if constexpr (XF32) {
+                const uint32_t q[8] = {s.x[i][0].x, s.x[i][0].y, s.x[i][0].z, s.x[i][0].w,
+                                       s.x[i][1].x, s.x[i][1].y, s.x[i][1].z, s.x[i][1].w};
+                uint32_t p[8][3];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dn_split3(__builtin_bit_cast(float, q[e]), p[e]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const u32x4 v = {p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16), p[4][k] | (p[5][k] << 16),
+                                     p[6][k] | (p[7][k] << 16)};
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, v), acc, 0, 0, 0);
+                }
+            } else {
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, s.x[i][0]), acc, 0, 0, 0);
+            }
+        }
+    };
+    RwSet<XF32> a, b;
+    load(a, 0);
+    for (int i0 = 0; i0 < per; i0 += 2 * RW_U) {
+        if (i0 + RW_U < per) load(b, i0 + RW_U);
+        multiply(a);
+        if (i0 + RW_U < per) {
+            if (i0 + 2 * RW_U < per) load(a, i0 + 2 * RW_U);
+            multiply(b);
+        }
+    }
+    // D: rows 4 lg + v (weight rows), column li (activation row)
+    if (HALVES == 1 || (li >> 3) == (lg >> 1))
+        *(float4v *)&s_part[wave * HALVES + half][r][HALVES == 2 ? 4 * (lg & 1) : 4 * lg] = acc;
+    __syncthreads();
+    constexpr int Q = RN / 4;  // four columns per thread
+    const int m = tid / Q, c = tid % Q * 4;
+    if (m >= P.M || n0 + c >= P.N) return;
+    float v[4], u[4];
+    auto sum = [&](float(&o)[4], int col) {
+        float4v q = *(const float4v *)&s_part[0][m][col];
+#pragma unroll
+        for (int p = 1; p < PARTS; ++p) q += *(const float4v *)&s_part[p][m][col];
+        o[0] = q.x;
+        o[1] = q.y;
+        o[2] = q.z;
+        o[3] = q.w;
+    };
+    sum(v, c);
+    if constexpr (GATED) {
+        sum(u, RN + c);
+        dn_epi_gated<4, DN_ACT_ANY>(P.e, P.M, P.N, m, n0 + c, v, u);
+    } else {
+        dn_epi_linear<4, DN_ACT_ANY>(P.e, P.N, m, n0 + c, v);
+    }
+}
+
+template <int EPI>
+static hipError_t rows_t(const DenseRowsParams &P, hipStream_t st) {
+    const int cols = EPI == DN_EPI_GATED ? 8 : 16;  // of a workgroup of 16 weight rows
+    const int64_t wgs = ((int64_t)P.N + cols - 1) / cols;
+    // 8 weight rows a workgroup while that leaves at most two per CU
+    const bool halves = P.M <= 8 && wgs <= 256;
+    const dim3 grid((unsigned)(halves ? ((int64_t)P.N + cols / 2 - 1) / (cols / 2) : wgs)), block(RW_WAVES * 64);
+    if (P.a_f32) {
+        if (halves)
+            hipLaunchKernelGGL((k_dense_rows<EPI, 1, 2>), grid, block, 0, st, P);
+        else
+            hipLaunchKernelGGL((k_dense_rows<EPI, 1, 1>), grid, block, 0, st, P);
+    } else {
+        if (halves)
+            hipLaunchKernelGGL((k_dense_rows<EPI, 0, 2>), grid, block, 0, st, P);
+        else
+            hipLaunchKernelGGL((k_dense_rows<EPI, 0, 1>), grid, block, 0, st, P);
+    }
+    return hipGetLastError();
+}
+
+hipError_t dense_rows_linear_launch(const DenseRowsParams &P, hipStream_t st) { return rows_t<DN_EPI_LINEAR>(P, st); }
+hipError_t dense_rows_gated_launch(const DenseRowsParams &P, hipStream_t st) { return rows_t<DN_EPI_GATED>(P, st); }
+
+}  // namespace moe
