@@ -33,7 +33,7 @@ namespace {
 constexpr int DN_MAX_WIDTH = 1 << 20;
 constexpr int DN_MAX_ROWS = 1 << 24;
 constexpr int DN_SPLIT_TILES = 512;  // tiles of a split product over all its splits
-constexpr int DN_DZ_CHUNKS = 256;  // row chunks of the bias gradient
+constexpr int DN_DZ_CHUNKS = 64;  // row chunks of the bias gradient
 
 int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -91,6 +91,12 @@ Plan make_plan(int64_t M, int64_t N, int64_t steps) {
     }
     return best;
 }
+#ifdef DN_FORCE
+extern "C" int g_force_rows;
+bool few_rows(int64_t T) { return g_force_rows >= 0 ? T <= g_force_rows : T <= DN_ROWS_MAX; }
+#else
+bool few_rows(int64_t T) { return T <= DN_ROWS_MAX; }
+#endif
 int64_t ksteps(int64_t K) { return ceil_div(K, DN_BK); }
 
 struct Carve {  // workspace regions after the head
@@ -186,6 +192,8 @@ int x_segments(DenseParams &P, const void *x, bool x_f32, int64_t T, int64_t K, 
 
 extern "C" {
 #ifdef DN_FORCE
+int g_force_rows = -1;
+void dn_force_rows(int r) { g_force_rows = r; }
 void dn_force(int tile, int split) { g_force_tile = tile; g_force_split = split; }
 #endif
 
@@ -224,7 +232,7 @@ int moe_linear(const void *x, int32_t x_dtype, int32_t T, int32_t in, const void
     e.y_f32 = y_dtype == MOE_DTYPE_F32;
     e.z = (uint16_t *)z;
     e.act = act;
-    if (T <= DN_ROWS_MAX) {
+    if (few_rows(T)) {
         const DenseRowsParams R{x, (const uint16_t *)w, nullptr, e, T, out, in, xf};
         return launch_err(dense_rows_linear_launch(R, S(stream)));
     }
@@ -345,7 +353,7 @@ int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn
     ed.res_f32 = r_dtype == MOE_DTYPE_F32;
     ed.y = y;
     ed.y_f32 = yf;
-    if (T <= DN_ROWS_MAX) {
+    if (few_rows(T)) {
         if (yf) eg.h_terms = 0;  // (fp32, split where it is read)
         const DenseRowsParams G{x, (const uint16_t *)w->gate, (const uint16_t *)w->up, eg, T, F, H, xf};
         if (dense_rows_gated_launch(G, st) != hipSuccess) return MOE_ERR_LAUNCH;

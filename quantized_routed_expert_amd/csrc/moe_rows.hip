@@ -1,10 +1,10 @@
-// moe_rows.hip -- C = A B^T for a decode window (M <= 16 rows): the weights
+// moe_rows.hip -- C = A B^T for few rows (M <= 64): the weights
 // are read once, straight into the registers that the MFMA takes, and nothing
 // else costs: bound by the weights' bytes and, below some 10 MB, by the launch
 // and one round trip to memory.
 //
 // One workgroup takes 16 weight rows (8 with HALVES = 2), its 8 waves a part
-// of K each.  v_mfma_f32_16x16x32_bf16: the weight rows are the row operand,
+// of K each, for MT blocks of 16 activation rows.  v_mfma_f32_16x16x32_bf16: the weight rows are the row operand,
 // the activation rows the column operand.  With HALVES = 2 (M <= 8) operand
 // rows 8..15 are the same 8 weight rows at another part of K and columns
 // 8..15 the same activations there; the two diagonal blocks of the result are
@@ -18,89 +18,110 @@
 namespace moe {
 
 constexpr int RW_WAVES = 8;
-constexpr int RW_U = 8;  // 32-k loads in flight per wave (two such sets)
+// 32-k loads of a set in flight per wave (two such sets), for MT blocks of 16
+// activation rows: what the registers hold
+template <int XF32, int MT>
+constexpr int RW_U = MT == 1 ? 8 : MT == 2 ? (XF32 ? 3 : 4) : (XF32 ? 2 : 3);
 
-template <int XF32>
+template <int XF32, int MT>
 struct RwSet {
-    u32x4 w[RW_U], x[RW_U][XF32 ? 2 : 1];
+    u32x4 w[RW_U<XF32, MT>], x[RW_U<XF32, MT>][MT][XF32 ? 2 : 1];
 };
 
-template <int EPI, int XF32, int HALVES>
+template <int EPI, int XF32, int HALVES, int MT>
 __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P) {
     constexpr bool GATED = EPI == DN_EPI_GATED;
     constexpr int R = 16 / HALVES;             // weight rows per workgroup
     constexpr int RN = GATED ? R / 2 : R;      // output columns per workgroup
     constexpr int PARTS = RW_WAVES * HALVES;
-    __shared__ __align__(16) float s_part[PARTS][16 / HALVES][R + 4];
+    constexpr int U = RW_U<XF32, MT>;
+    static_assert(HALVES == 1 || MT == 1, "one block of 8 rows");
+    __shared__ __align__(16) float s_part[PARTS][MT * 16 / HALVES][R + 4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int half = HALVES == 2 ? li >> 3 : 0, r = HALVES == 2 ? li & 7 : li;
     const int n0 = blockIdx.x * RN;
     // rows past the end read a valid row and are never stored
-    const int n = min(n0 + (GATED ? r % RN : r), P.N - 1), t = min(r, P.M - 1);
+    const int n = min(n0 + (GATED ? r % RN : r), P.N - 1);
     const uint16_t *wr = (GATED && r >= RN ? P.b2 : P.b) + (int64_t)n * P.K;
     // this lane's part of K: 32-k pieces from k0 on
     const int pieces = (P.K + 31) / 32, per = (pieces + PARTS - 1) / PARTS;
     const int k0 = (wave * HALVES + half) * per * 32 + 8 * lg;
 
-    auto load = [&](RwSet<XF32> &s, int i0) {
+    auto load = [&](RwSet<XF32, MT> &s, int i0) {
 #pragma unroll
-        for (int i = 0; i < RW_U; ++i) {
+        for (int i = 0; i < U; ++i) {
             const int k = k0 + (i0 + i) * 32;
             // (a piece past the part or past K is zero in both operands)
             const bool in = i0 + i < per && k < P.K;
             const u32x4 z = {0u, 0u, 0u, 0u};
             s.w[i] = z;
-            s.x[i][0] = z;
-            if (XF32) s.x[i][XF32] = z;
+#pragma unroll
+            for (int q = 0; q < MT; ++q) {
+                s.x[i][q][0] = z;
+                if (XF32) s.x[i][q][XF32] = z;
+            }
             if (in) {
                 s.w[i] = *(const u32x4 *)(wr + k);
-                if constexpr (XF32) {
-                    const float *xr = (const float *)P.a + (int64_t)t * P.K + k;
-                    s.x[i][0] = *(const u32x4 *)xr;
-                    s.x[i][1] = *(const u32x4 *)(xr + 4);
-                } else {
-                    s.x[i][0] = *(const u32x4 *)((const uint16_t *)P.a + (int64_t)t * P.K + k);
+#pragma unroll
+                for (int q = 0; q < MT; ++q) {
+                    const int64_t at = (int64_t)min(16 * q + r, P.M - 1) * P.K + k;
+                    if constexpr (XF32) {
+                        s.x[i][q][0] = *(const u32x4 *)((const float *)P.a + at);
+                        s.x[i][q][1] = *(const u32x4 *)((const float *)P.a + at + 4);
+                    } else {
+                        s.x[i][q][0] = *(const u32x4 *)((const uint16_t *)P.a + at);
+                    }
                 }
             }
         }
     };
-    float4v acc = {0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const RwSet<XF32> &s) {
+    float4v acc[MT];
 #pragma unroll
-        for (int i = 0; i < RW_U; ++i) {
+    for (int q = 0; q < MT; ++q) acc[q] = float4v{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const RwSet<XF32, MT> &s, int i0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (i0 + i >= per) break;  // (uniform: a short part)
             const bf16x8 w = __builtin_bit_cast(bf16x8, s.w[i]);
-            if constexpr (XF32) {
-                const uint32_t q[8] = {s.x[i][0].x, s.x[i][0].y, s.x[i][0].z, s.x[i][0].w,
-                                       s.x[i][1].x, s.x[i][1].y, s.x[i][1].z, s.x[i][1].w};
-                uint32_t p[8][3];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dn_split3(__builtin_bit_cast(float, q[e]), p[e]);
+            for (int q = 0; q < MT; ++q) {
+                const u32x4 x0 = s.x[i][q][0];
+                if constexpr (XF32) {
+                    const u32x4 x1 = s.x[i][q][1];
+                    const uint32_t f[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                    uint32_t p[8][3];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const u32x4 v = {p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16), p[4][k] | (p[5][k] << 16),
-                                     p[6][k] | (p[7][k] << 16)};
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, v), acc, 0, 0, 0);
+                    for (int e = 0; e < 8; ++e) dn_split3(__builtin_bit_cast(float, f[e]), p[e]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const u32x4 v = {p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16), p[4][k] | (p[5][k] << 16),
+                                         p[6][k] | (p[7][k] << 16)};
+                        acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, v), acc[q], 0, 0, 0);
+                    }
+                } else {
+                    acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x0), acc[q], 0, 0, 0);
                 }
-            } else {
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, s.x[i][0]), acc, 0, 0, 0);
             }
         }
     };
-    RwSet<XF32> a, b;
+    RwSet<XF32, MT> a, b;
     load(a, 0);
-    for (int i0 = 0; i0 < per; i0 += 2 * RW_U) {
-        if (i0 + RW_U < per) load(b, i0 + RW_U);
-        multiply(a);
-        if (i0 + RW_U < per) {
-            if (i0 + 2 * RW_U < per) load(a, i0 + 2 * RW_U);
-            multiply(b);
+    for (int i0 = 0; i0 < per; i0 += 2 * U) {
+        if (i0 + U < per) load(b, i0 + U);
+        multiply(a, i0);
+        if (i0 + U < per) {
+            if (i0 + 2 * U < per) load(a, i0 + 2 * U);
+            multiply(b, i0 + U);
         }
     }
     // D: rows 4 lg + v (weight rows), column li (activation row)
-    if (HALVES == 1 || (li >> 3) == (lg >> 1))
-        *(float4v *)&s_part[wave * HALVES + half][r][HALVES == 2 ? 4 * (lg & 1) : 4 * lg] = acc;
+    if (HALVES == 1 || (li >> 3) == (lg >> 1)) {
+#pragma unroll
+        for (int q = 0; q < MT; ++q)
+            *(float4v *)&s_part[wave * HALVES + half][16 * q + r][HALVES == 2 ? 4 * (lg & 1) : 4 * lg] = acc[q];
+    }
     __syncthreads();
     constexpr int Q = RN / 4;  // four columns per thread
     const int m = tid / Q, c = tid % Q * 4;
@@ -131,17 +152,27 @@ static hipError_t rows_t(const DenseRowsParams &P, hipStream_t st) {
     // 8 weight rows a workgroup while that leaves at most two per CU
     const bool halves = P.M <= 8 && wgs <= 256;
     const dim3 grid((unsigned)(halves ? ((int64_t)P.N + cols / 2 - 1) / (cols / 2) : wgs)), block(RW_WAVES * 64);
+#define RW_LAUNCH(XF32, HALVES, MT) hipLaunchKernelGGL((k_dense_rows<EPI, XF32, HALVES, MT>), grid, block, 0, st, P)
     if (P.a_f32) {
         if (halves)
-            hipLaunchKernelGGL((k_dense_rows<EPI, 1, 2>), grid, block, 0, st, P);
+            RW_LAUNCH(1, 2, 1);
+        else if (P.M <= 16)
+            RW_LAUNCH(1, 1, 1);
+        else if (P.M <= 32)
+            RW_LAUNCH(1, 1, 2);
         else
-            hipLaunchKernelGGL((k_dense_rows<EPI, 1, 1>), grid, block, 0, st, P);
+            RW_LAUNCH(1, 1, 4);
     } else {
         if (halves)
-            hipLaunchKernelGGL((k_dense_rows<EPI, 0, 2>), grid, block, 0, st, P);
+            RW_LAUNCH(0, 2, 1);
+        else if (P.M <= 16)
+            RW_LAUNCH(0, 1, 1);
+        else if (P.M <= 32)
+            RW_LAUNCH(0, 1, 2);
         else
-            hipLaunchKernelGGL((k_dense_rows<EPI, 0, 1>), grid, block, 0, st, P);
+            RW_LAUNCH(0, 1, 4);
     }
+#undef RW_LAUNCH
     return hipGetLastError();
 }
 
