@@ -105,33 +105,33 @@ __device__ __forceinline__ void dn_store_f32(float *p, const float (&v)[V]) {
     for (int i = 0; i < V; i += 4) *(float4v *)(p + i) = float4v{v[i], v[i + 1], v[i + 2], v[i + 3]};
 }
 
-// An fp32 value as three bf16 terms: 8 significant bits each, cut toward
-// zero, so the terms sum to the value exactly (24 bits) unless the last ones
-// underflow.  Infinities and NaN stay in the first term alone.
+// An fp32 value as three bf16 terms (each in the high half of t[i]): 8
+// significant bits each, cut toward zero, so the terms sum to the value
+// exactly (24 bits) unless the last ones underflow.  An infinity or NaN stays
+// in the first term alone (canonicalized: a NaN keeps its high mantissa bit).
 __device__ __forceinline__ void dn_split3(float v, uint32_t (&t)[3]) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    if ((u & 0x7F800000u) == 0x7F800000u) {
-        t[0] = (u >> 16) | ((u & 0x007FFFFFu) ? 0x40u : 0u);  // (a NaN keeps a mantissa bit)
-        t[1] = t[2] = 0u;
-        return;
-    }
-    t[0] = u >> 16;
-    const float r1 = v - __builtin_bit_cast(float, u & 0xFFFF0000u);  // exact
-    const uint32_t u1 = __builtin_bit_cast(uint32_t, r1);
-    t[1] = u1 >> 16;
-    const float r2 = r1 - __builtin_bit_cast(float, u1 & 0xFFFF0000u);  // exact, at most 8 bits
-    t[2] = __builtin_bit_cast(uint32_t, r2) >> 16;
+    v = __builtin_canonicalizef(v);
+    t[0] = __builtin_bit_cast(uint32_t, v);
+    float r = v - __builtin_bit_cast(float, t[0] & 0xFFFF0000u);  // exact
+    r = __builtin_fabsf(v) < __builtin_inff() ? r : 0.0f;
+    t[1] = __builtin_bit_cast(uint32_t, r);
+    t[2] = __builtin_bit_cast(uint32_t, r - __builtin_bit_cast(float, t[1] & 0xFFFF0000u));  // exact, at most 8 bits
 }
+// the high halves of a and b: two bf16
+__device__ __forceinline__ uint32_t dn_high2(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 template <int V>
 __device__ __forceinline__ void dn_store_split3(uint16_t *p, size_t plane, const float (&v)[V]) {
     uint32_t t[V][3];
 #pragma unroll
     for (int i = 0; i < V; ++i) dn_split3(v[i], t[i]);
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int i = 0; i < V; i += 4)
-            *(u32x2 *)(p + k * plane + i) = u32x2{t[i][k] | (t[i + 1][k] << 16), t[i + 2][k] | (t[i + 3][k] << 16)};
+    for (int k = 0; k < 3; ++k) {
+        if constexpr (V == 8)
+            *(u32x4 *)(p + k * plane) = u32x4{dn_high2(t[0][k], t[1][k]), dn_high2(t[2][k], t[3][k]),
+                                              dn_high2(t[4][k], t[5][k]), dn_high2(t[6][k], t[7][k])};
+        else
+            *(u32x2 *)(p + k * plane) = u32x2{dn_high2(t[0][k], t[1][k]), dn_high2(t[2][k], t[3][k])};
+    }
 }
 
 // ---------------------------------------------------------------------------

@@ -4,8 +4,8 @@
 // and one round trip to memory.
 //
 // One workgroup takes 16 weight rows (8 with HALVES = 2), its 8 waves a part
-// of K each, for MT blocks of 16 activation rows.  v_mfma_f32_16x16x32_bf16: the weight rows are the row operand,
-// the activation rows the column operand.  With HALVES = 2 (M <= 8) operand
+// of K each, for MT blocks of 16 activation rows (8 with HALVES = 2).  v_mfma_f32_16x16x32_bf16: the weight rows are the row operand,
+// the activation rows the column operand.  With HALVES = 2 operand
 // rows 8..15 are the same 8 weight rows at another part of K and columns
 // 8..15 the same activations there; the two diagonal blocks of the result are
 // the two parts' sums, so no lane loads a byte twice and twice as many
@@ -21,7 +21,7 @@ constexpr int RW_WAVES = 8;
 // 32-k loads of a set in flight per wave (two such sets), for MT blocks of 16
 // activation rows: what the registers hold
 template <int XF32, int MT>
-constexpr int RW_U = MT == 1 ? 8 : MT == 2 ? (XF32 ? 3 : 4) : (XF32 ? 2 : 3);
+constexpr int RW_U = MT == 1 ? 6 : MT == 2 ? (XF32 ? 3 : 4) : (XF32 ? 2 : 3);
 
 template <int XF32, int MT>
 struct RwSet {
@@ -35,7 +35,6 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
     constexpr int RN = GATED ? R / 2 : R;      // output columns per workgroup
     constexpr int PARTS = RW_WAVES * HALVES;
     constexpr int U = RW_U<XF32, MT>;
-    static_assert(HALVES == 1 || MT == 1, "one block of 8 rows");
     __shared__ __align__(16) float s_part[PARTS][MT * 16 / HALVES][R + 4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -66,7 +65,7 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
                 s.w[i] = *(const u32x4 *)(wr + k);
 #pragma unroll
                 for (int q = 0; q < MT; ++q) {
-                    const int64_t at = (int64_t)min(16 * q + r, P.M - 1) * P.K + k;
+                    const int64_t at = (int64_t)min(16 / HALVES * q + r, P.M - 1) * P.K + k;
                     if constexpr (XF32) {
                         s.x[i][q][0] = *(const u32x4 *)((const float *)P.a + at);
                         s.x[i][q][1] = *(const u32x4 *)((const float *)P.a + at + 4);
@@ -96,8 +95,8 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
                     for (int e = 0; e < 8; ++e) dn_split3(__builtin_bit_cast(float, f[e]), p[e]);
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
-                        const u32x4 v = {p[0][k] | (p[1][k] << 16), p[2][k] | (p[3][k] << 16), p[4][k] | (p[5][k] << 16),
-                                         p[6][k] | (p[7][k] << 16)};
+                        const u32x4 v = {dn_high2(p[0][k], p[1][k]), dn_high2(p[2][k], p[3][k]), dn_high2(p[4][k], p[5][k]),
+                                         dn_high2(p[6][k], p[7][k])};
                         acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, v), acc[q], 0, 0, 0);
                     }
                 } else {
@@ -120,7 +119,7 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
     if (HALVES == 1 || (li >> 3) == (lg >> 1)) {
 #pragma unroll
         for (int q = 0; q < MT; ++q)
-            *(float4v *)&s_part[wave * HALVES + half][16 * q + r][HALVES == 2 ? 4 * (lg & 1) : 4 * lg] = acc[q];
+            *(float4v *)&s_part[wave * HALVES + half][16 / HALVES * q + r][HALVES == 2 ? 4 * (lg & 1) : 4 * lg] = acc[q];
     }
     __syncthreads();
     constexpr int Q = RN / 4;  // four columns per thread
@@ -150,12 +149,14 @@ static hipError_t rows_t(const DenseRowsParams &P, hipStream_t st) {
     const int cols = EPI == DN_EPI_GATED ? 8 : 16;  // of a workgroup of 16 weight rows
     const int64_t wgs = ((int64_t)P.N + cols - 1) / cols;
     // 8 weight rows a workgroup while that leaves at most two per CU
-    const bool halves = P.M <= 8 && wgs <= 256;
+    const bool halves = P.M <= 16 && wgs <= 256;
     const dim3 grid((unsigned)(halves ? ((int64_t)P.N + cols / 2 - 1) / (cols / 2) : wgs)), block(RW_WAVES * 64);
 #define RW_LAUNCH(XF32, HALVES, MT) hipLaunchKernelGGL((k_dense_rows<EPI, XF32, HALVES, MT>), grid, block, 0, st, P)
     if (P.a_f32) {
-        if (halves)
+        if (halves && P.M <= 8)
             RW_LAUNCH(1, 2, 1);
+        else if (halves)
+            RW_LAUNCH(1, 2, 2);
         else if (P.M <= 16)
             RW_LAUNCH(1, 1, 1);
         else if (P.M <= 32)
@@ -163,8 +164,10 @@ static hipError_t rows_t(const DenseRowsParams &P, hipStream_t st) {
         else
             RW_LAUNCH(1, 1, 4);
     } else {
-        if (halves)
+        if (halves && P.M <= 8)
             RW_LAUNCH(0, 2, 1);
+        else if (halves)
+            RW_LAUNCH(0, 2, 2);
         else if (P.M <= 16)
             RW_LAUNCH(0, 1, 1);
         else if (P.M <= 32)
