@@ -428,9 +428,12 @@ struct DnCursor {
 // its own part of the tile's steps; their sums are added in LDS, in order, at
 // the end.  Small tiles spend their time waiting for loads; the groups keep
 // KG times as many in flight and take 1 / KG of the steps.
+template <int BM, int BN, int KG>
+constexpr int DN_LDS = KG * (2 * BM + 3 * BN) * 128;
+
+#ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the kernels' stubs alone: it drops those that use the buffer builtins)
 template <int BM, int BN, int WM, int WN, int KG, int FORM, int EPI, int ACT>
-__global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(DenseParams P) {
-#ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the stub alone: it drops stubs of templates that use the buffer builtins)
+__device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int split, uint8_t *smem) {
     constexpr int NW = WM * WN;  // waves per group
     constexpr bool AKC = FORM != DN_TN, BKC = FORM == DN_NT;
     constexpr bool GATED = EPI == DN_EPI_GATED;
@@ -440,8 +443,8 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
     typedef DnStream<BM, AKC, NW> SA;
     typedef DnStream<BN, BKC, NW> SB;
     constexpr int RING = 2 * SA::BYTES + 3 * SB::BYTES;
+    static_assert(RING * KG == DN_LDS<BM, BN, KG>, "slices");
     static_assert(KG == 1 || BM * BN * 4 <= RING, "the groups' sums fit the slices");
-    __shared__ __align__(1024) uint8_t smem[RING * KG];
     lds_u8 *const lds_all = (lds_u8 *)smem;
 
     const int lane = threadIdx.x & 63;
@@ -451,13 +454,13 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
     const int wm = wave / WN, wn = wave % WN;
     lds_u8 *const lds = lds_all + grp * RING;
     int tm, tn;
-    dn_tile(P, blockIdx.x, tm, tn);
+    dn_tile(P, tile, tm, tn);
     const int64_t m0 = (int64_t)tm * BM;
     constexpr int BNF = GATED ? BN / 2 : BN;  // output columns per tile
     const int64_t n0 = (int64_t)tn * BNF;
     const int rows = (int)min((int64_t)BM, P.M - m0), cols = (int)min((int64_t)BNF, P.N - n0);
     // this group's steps (a group past the end multiplies zeros)
-    const int s_wg = (int)blockIdx.y * P.steps_per_split, e_wg = min(P.steps, s_wg + P.steps_per_split);
+    const int s_wg = split * P.steps_per_split, e_wg = min(P.steps, s_wg + P.steps_per_split);
     const int nstep = KG > 1 ? (e_wg - s_wg + KG - 1) / KG : e_wg - s_wg;
     const int s0 = s_wg + grp * nstep;
 
@@ -637,7 +640,7 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
                     u[p] = block(j0 + 2 * p + 1);
                 }
                 if (P.splits > 1) {
-                    float *const part = P.part + ((int64_t)blockIdx.y * P.M + m) * (2 * (int64_t)P.N);
+                    float *const part = P.part + ((int64_t)split * P.M + m) * (2 * (int64_t)P.N);
 #pragma unroll
                     for (int p = 0; p < JP; ++p) {
                         const int n = nb + 16 * p + 4 * lg;
@@ -661,7 +664,7 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
                 const int nb = (int)n0 + b_row + 32 * uj;
                 const float4v v0 = block(2 * uj), v1 = block(2 * uj + 1);
                 if (P.splits > 1) {
-                    float *const part = P.part + ((int64_t)blockIdx.y * P.M + m) * P.N;
+                    float *const part = P.part + ((int64_t)split * P.M + m) * P.N;
                     const int n = nb + 4 * lg;
                     if (m < P.M && n < P.N) *(float4v *)(part + n) = v0;
                     if (m < P.M && n + 16 < P.N) *(float4v *)(part + n + 16) = v1;
@@ -680,6 +683,31 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
             }
         }
     }
+}
+#endif
+
+template <int BM, int BN, int WM, int WN, int KG, int FORM, int EPI, int ACT>
+__global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(DenseParams P) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG>];
+    dense_body<BM, BN, WM, WN, KG, FORM, EPI, ACT>(P, blockIdx.x, blockIdx.y, smem);
+#endif
+}
+
+// A backward pass's last products, which do not depend on each other, in one
+// launch: the input gradient (A B) and up to two weight gradients (A^T B), the
+// one with the longest tiles first.  Apart they would each end in a round of
+// tiles that leaves CUs idle, and wait for the launch before them.
+template <int BM, int BN, int WM, int WN, int KG>
+__global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense_grads(DenseGradsParams A) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG>];
+    int b = blockIdx.x, i = 0;
+    while (b >= A.tiles[i]) b -= A.tiles[i++];  // (the grid is the sum of the tiles)
+    if (A.which[i] == 0)
+        dense_body<BM, BN, WM, WN, KG, DN_NN, DN_EPI_LINEAR, DN_ACT_NONE>(A.dx, b, 0, smem);
+    else
+        dense_body<BM, BN, WM, WN, KG, DN_TN, DN_EPI_GRAD, DN_ACT_NONE>(A.dw[A.which[i] - 1], b, 0, smem);
 #endif
 }
 
@@ -715,25 +743,23 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseParams P) {
     }
 }
 
+// launch(tile shape...) for a tile
+#define DN_TILE_SWITCH(tile, LAUNCH)                             \
+    switch (tile) {                                              \
+        case DN_TILE_256x256: LAUNCH(512, 256, 256, 2, 4, 1); break; \
+        case DN_TILE_256x128: LAUNCH(512, 256, 128, 4, 2, 1); break; \
+        case DN_TILE_128x128: LAUNCH(512, 128, 128, 2, 2, 2); break; \
+        case DN_TILE_64x64: LAUNCH(1024, 64, 64, 2, 2, 4); break;    \
+        default: return hipErrorInvalidValue;                    \
+    }
+
 // One product of the given form and epilogue, and its join when it is split.
 template <int FORM, int EPI, int ACT>
 hipError_t dense_tile_t(const DenseParams &P, int tile, hipStream_t st) {
     const dim3 grid((unsigned)(P.tiles_m * P.tiles_n), (unsigned)P.splits);
-    switch (tile) {
-        case DN_TILE_256x256:
-            hipLaunchKernelGGL((k_dense<256, 256, 2, 4, 1, FORM, EPI, ACT>), grid, dim3(512), 0, st, P);
-            break;
-        case DN_TILE_256x128:
-            hipLaunchKernelGGL((k_dense<256, 128, 4, 2, 1, FORM, EPI, ACT>), grid, dim3(512), 0, st, P);
-            break;
-        case DN_TILE_128x128:
-            hipLaunchKernelGGL((k_dense<128, 128, 2, 2, 2, FORM, EPI, ACT>), grid, dim3(512), 0, st, P);
-            break;
-        case DN_TILE_64x64:
-            hipLaunchKernelGGL((k_dense<64, 64, 2, 2, 4, FORM, EPI, ACT>), grid, dim3(1024), 0, st, P);
-            break;
-        default: return hipErrorInvalidValue;
-    }
+#define DN_LAUNCH(THREADS, ...) hipLaunchKernelGGL((k_dense<__VA_ARGS__, FORM, EPI, ACT>), grid, dim3(THREADS), 0, st, P)
+    DN_TILE_SWITCH(tile, DN_LAUNCH)
+#undef DN_LAUNCH
     return hipGetLastError();
 }
 template <int FORM, int EPI>

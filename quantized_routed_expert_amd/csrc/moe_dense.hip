@@ -18,6 +18,7 @@ hipError_t dense_gated_launch(const DenseParams &P, int tile, hipStream_t st);
 hipError_t dense_dgated_launch(const DenseParams &P, int tile, hipStream_t st);
 hipError_t dense_dx_launch(const DenseParams &P, int tile, hipStream_t st);
 hipError_t dense_dw_launch(const DenseParams &P, int tile, hipStream_t st);
+hipError_t dense_grads_launch(const DenseGradsParams &A, int tile, hipStream_t st);
 hipError_t dense_rows_linear_launch(const DenseRowsParams &P, hipStream_t st);
 hipError_t dense_rows_gated_launch(const DenseRowsParams &P, hipStream_t st);
 }  // namespace moe
@@ -54,23 +55,35 @@ bool misaligned(const void *p) { return ((uintptr_t)p & 15) != 0; }
 // ---- tile and split choice ----
 struct Plan {
     int tile, tiles_m, tiles_n, splits, per;
+    double us;  // estimated time
 };
-// Tile and split: the least estimated time over the tiles and split counts.
-// A launch takes rounds of one tile per CU; a tile takes a fixed time and one
-// per step (of its longest group), a split adds the parts' traffic and the
-// joining launch.
+// The least estimated time over the tiles and split counts.  Rounds of one
+// tile per CU; a tile takes a fixed time and one per step (of its longest
+// group), the results one per MB, a split the joining launch and the parts'
+// traffic.  Fitted to 380 launches of 51 products (64 x 2048 x 2048 to
+// 8192 x 4096 x 11008, each tile, splits of 1 to 8; 9% off in the mean; the
+// choice costs 0.5% over the best of each): e.g. 2048 x 2048 outputs over 512 k
+// take 10 us in 128 x 128 tiles and 20 in 64 x 64, 2048 x 512 outputs over
+// 2048 k 18 and 10.
 struct TileCost {
     int bm, bn, groups;
     double fixed, step;  // us
 };
-constexpr TileCost TILES[DN_TILES] = {{256, 256, 1, 9.0, 1.36}, {256, 128, 1, 6.0, 0.75}, {128, 128, 2, 5.0, 0.9}, {64, 64, 4, 4.0, 0.6}};
+constexpr TileCost TILES[DN_TILES] = {
+    {256, 256, 1, 5.1, 1.10}, {256, 128, 1, 2.6, 0.68}, {128, 128, 2, 2.7, 0.78}, {64, 64, 4, 2.3, 0.74}};
+constexpr double US_LAUNCH = 1.5, US_JOIN = 4.9, US_PER_MB = 0.16, US_PER_PART_MB = 0.67;
+constexpr int CUS = 256;  // (workspace sizes do not depend on the device at hand)
+
+double tile_us(const TileCost &c, int64_t steps) { return c.fixed + c.step * (double)ceil_div(steps, c.groups); }
+double out_us(int64_t M, int64_t N) { return (double)M * (double)N * 2e-6 * US_PER_MB; }
+
 #ifdef DN_FORCE
-int g_force_tile = -1, g_force_split = 1;
+int g_force_tile = -1, g_force_split = 1, g_force_rows = -1;
 #endif
 // C of M x N columns of the weight side (gated: 2F) over `steps` 64-k steps
 Plan make_plan(int64_t M, int64_t N, int64_t steps) {
-    Plan best = {-1, 0, 0, 1, 1};
-    double best_t = 1e30;
+    Plan best = {-1, 0, 0, 1, 1, 1e30};
+    steps = max64(steps, 1);
     for (int t = 0; t < DN_TILES; ++t) {
         const TileCost &c = TILES[t];
         const int64_t tm = ceil_div(M, c.bm), tn = ceil_div(N, c.bn), tiles = max64(tm * tn, 1);  // (M = 0: nothing is launched)
@@ -79,24 +92,38 @@ Plan make_plan(int64_t M, int64_t N, int64_t steps) {
             if (g_force_tile >= 0 && (t != g_force_tile || s != g_force_split)) continue;
 #endif
             if (s > 1 && (tiles * s * c.bm * c.bn > (int64_t)DN_SPLIT_TILES * 128 * 128 || steps < 4 * s * c.groups)) break;
-            const int64_t per = ceil_div(max64(steps, 1), s);
-            const double rounds = (double)ceil_div(tiles * s, 256);
-            double us = rounds * (c.fixed + c.step * (double)ceil_div(per, c.groups));
-            if (s > 1) us += 6.0 + (double)(s * M * N) * 8.0 / 4.0e6;
-            if (us < best_t) {
-                best_t = us;
-                best = Plan{t, (int)tm, (int)tn, (int)ceil_div(max64(steps, 1), per), (int)per};
-            }
+            const int64_t per = ceil_div(steps, s);
+            double us = US_LAUNCH + (double)ceil_div(tiles * s, CUS) * tile_us(c, per) + out_us(M, N);
+            if (s > 1) us += US_JOIN + (double)s * (double)M * (double)N * 4e-6 * US_PER_PART_MB;
+            if (us < best.us) best = Plan{t, (int)tm, (int)tn, (int)ceil_div(steps, per), (int)per, us};
         }
     }
     return best;
 }
+
+// The few-row kernel against tiles: a workgroup takes 16 weight rows (8 up to
+// 16 activation rows while that is at most two per CU) and reads its
+// activation rows from L2, together 35 KB a microsecond; all weights at most
+// 5.1 TB/s.  (T, K, N = 16, 2048, 2048: 5.3 us and 8.4 with tiles; 16, 2048,
+// 11264: 13.8 and 11.2; 64, 2048, 2048: 11.3 and 8.8; 37, 1000, 520: 4.2 and
+// 6.4.)
+double rows_us(int64_t T, int64_t K, int64_t rows, bool x_f32) {
+    const bool halves = T <= 16 && ceil_div(rows, 16) <= CUS;
+    const int64_t wr = halves ? 8 : 16, wgs = ceil_div(rows, wr);
+    const int64_t xr = T == 1 ? 1 : ceil_div(T, wr) * wr;  // (one row: every lane's load is the same)
+    const double bytes = (double)K * (double)(2 * wr + (x_f32 ? 5 : 2) * xr);
+    const double rounds = wgs > CUS ? (double)wgs / CUS : 1.0;
+    const double us = rounds * bytes / 35e3, hbm = (double)K * (double)rows * 2.0 / 5.1e6;
+    return 2.3 + (us > hbm ? us : hbm);
+}
+bool few_rows(int64_t T, int64_t K, int64_t rows, bool x_f32, const Plan &tiles) {
+    if (T > DN_ROWS_MAX) return false;
 #ifdef DN_FORCE
-extern "C" int g_force_rows;
-bool few_rows(int64_t T) { return g_force_rows >= 0 ? T <= g_force_rows : T <= DN_ROWS_MAX; }
-#else
-bool few_rows(int64_t T) { return T <= DN_ROWS_MAX; }
+    if (g_force_rows >= 0) return T <= g_force_rows;
 #endif
+    return rows_us(T, K, rows, x_f32) < tiles.us + (x_f32 ? 2.7 : 0.0);  // (tiles: fp32 is split by a launch of its own)
+}
+
 int64_t ksteps(int64_t K) { return ceil_div(K, DN_BK); }
 
 struct Carve {  // workspace regions after the head
@@ -175,6 +202,72 @@ GatedWs gated_ws(int64_t T, int64_t H, int64_t F, bool x_f32, bool y_f32) {
 inline hipStream_t S(int64_t s) { return (hipStream_t)(intptr_t)s; }
 int launch_err(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 
+// A backward pass's last products, planned apart (pdx, pdw[0..n)): one launch
+// of all where its estimate is lower, else one each.
+int launch_grads(const DenseParams *dx, const Plan &pdx, DenseParams *const *dw, const Plan *pdw, int n, hipStream_t st) {
+    const DenseParams *all[3];
+    int which[3], k = 0;
+    double apart = 0.0;
+    if (dx) {
+        all[k] = dx;
+        which[k++] = 0;
+        apart += pdx.us;
+    }
+    for (int i = 0; i < n; ++i) {
+        all[k] = dw[i];
+        which[k++] = 1 + i;
+        apart += pdw[i].us;
+    }
+    // together: the tiles' times over the CUs, and half a tile for the last round
+    int best = -1;
+    double best_us = 1e30;
+    for (int t = 0; t < DN_TILES; ++t) {
+        const TileCost &c = TILES[t];
+        double sum = 0.0, out = 0.0, least = 1e30;
+        for (int i = 0; i < k; ++i) {
+            const double us = tile_us(c, all[i]->steps);
+            sum += us * (double)(ceil_div(all[i]->M, c.bm) * ceil_div(all[i]->N, c.bn));
+            out += out_us(all[i]->M, all[i]->N);
+            least = us < least ? us : least;
+        }
+        const double us = US_LAUNCH + out + (sum / CUS < least ? least : sum / CUS + 0.5 * least);
+        if (us < best_us) {
+            best_us = us;
+            best = t;
+        }
+    }
+    if (k < 2 || apart <= best_us) {
+        if (dx && dense_dx_launch(*dx, pdx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+        for (int i = 0; i < n; ++i)
+            if (dense_dw_launch(*dw[i], pdw[i].tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+        return MOE_OK;
+    }
+    DenseGradsParams A;
+    memset(&A, 0, sizeof(A));
+    for (int i = 0; i < k; ++i) {  // longest tiles first
+        for (int j = i; j > 0 && all[j]->steps > all[j - 1]->steps; --j) {
+            const DenseParams *p = all[j];
+            const int w = which[j];
+            all[j] = all[j - 1];
+            which[j] = which[j - 1];
+            all[j - 1] = p;
+            which[j - 1] = w;
+        }
+    }
+    const TileCost &c = TILES[best];
+    for (int i = 0; i < k; ++i) {
+        DenseParams &P = which[i] == 0 ? A.dx : A.dw[which[i] - 1];
+        P = *all[i];
+        P.tiles_m = (int)ceil_div(P.M, c.bm);
+        P.tiles_n = (int)ceil_div(P.N, c.bn);
+        P.splits = 1;
+        P.steps_per_split = P.steps > 0 ? P.steps : 1;
+        A.which[i] = which[i];
+        A.tiles[i] = P.tiles_m * P.tiles_n;
+    }
+    return launch_err(dense_grads_launch(A, best, st));
+}
+
 // x's products with rows of K: one (bf16) or three (fp32, its exact bf16
 // terms, written to x3 first)
 int x_segments(DenseParams &P, const void *x, bool x_f32, int64_t T, int64_t K, uint16_t *x3, hipStream_t st) {
@@ -192,7 +285,6 @@ int x_segments(DenseParams &P, const void *x, bool x_f32, int64_t T, int64_t K, 
 
 extern "C" {
 #ifdef DN_FORCE
-int g_force_rows = -1;
 void dn_force_rows(int r) { g_force_rows = r; }
 void dn_force(int tile, int split) { g_force_tile = tile; g_force_split = split; }
 #endif
@@ -232,7 +324,7 @@ int moe_linear(const void *x, int32_t x_dtype, int32_t T, int32_t in, const void
     e.y_f32 = y_dtype == MOE_DTYPE_F32;
     e.z = (uint16_t *)z;
     e.act = act;
-    if (few_rows(T)) {
+    if (few_rows(T, in, out, xf, L.fwd)) {
         const DenseRowsParams R{x, (const uint16_t *)w, nullptr, e, T, out, in, xf};
         return launch_err(dense_rows_linear_launch(R, S(stream)));
     }
@@ -288,28 +380,26 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
         ColsumParams C{(const float *)at(ws, L.chunks), dbias, out, nchunks, dw_dtype == MOE_DTYPE_F32, accumulate != 0};
         if (dense_colsum_launch(C, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
-    if (dx && T != 0) {
-        DenseParams P;
-        memset(&P, 0, sizeof(P));
-        P.nseg = 1;
-        P.seg[0] = DenseSeg{dz, (const uint16_t *)w, nullptr, out, in, out};
-        set_plan(P, L.dx, T, in, (int)ksteps(out), (float *)at(ws, L.bpart));
-        P.e.y = dx;
-        if (dense_dx_launch(P, L.dx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    DenseParams X, W, *const dws[1] = {&W};
+    memset(&X, 0, sizeof(X));
+    memset(&W, 0, sizeof(W));
+    const bool with_dx = dx && T != 0;
+    if (with_dx) {
+        X.nseg = 1;
+        X.seg[0] = DenseSeg{dz, (const uint16_t *)w, nullptr, out, in, out};
+        set_plan(X, L.dx, T, in, (int)ksteps(out), (float *)at(ws, L.bpart));
+        X.e.y = dx;
     }
     if (dw) {
-        DenseParams P;
-        memset(&P, 0, sizeof(P));
-        P.nseg = 1;
-        P.seg[0] = DenseSeg{dz, (const uint16_t *)x, nullptr, out, in, T};
-        set_plan(P, L.dw, out, in, (int)ksteps(T), (float *)at(ws, L.bpart));
-        P.e.y = dw;
-        P.e.m_split = out;
-        P.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
-        P.e.accumulate = accumulate != 0;
-        if (dense_dw_launch(P, L.dw.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+        W.nseg = 1;
+        W.seg[0] = DenseSeg{dz, (const uint16_t *)x, nullptr, out, in, T};
+        set_plan(W, L.dw, out, in, (int)ksteps(T), (float *)at(ws, L.bpart));
+        W.e.y = dw;
+        W.e.m_split = out;
+        W.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
+        W.e.accumulate = accumulate != 0;
     }
-    return MOE_OK;
+    return launch_grads(with_dx ? &X : nullptr, L.dx, dws, &L.dw, dw ? 1 : 0, st);
 }
 
 int64_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t hidden, int32_t ffn) {
@@ -353,24 +443,30 @@ int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn
     ed.res_f32 = r_dtype == MOE_DTYPE_F32;
     ed.y = y;
     ed.y_f32 = yf;
-    if (few_rows(T)) {
-        if (yf) eg.h_terms = 0;  // (fp32, split where it is read)
+    // h between the two: fp32 (split where it is read) for the few-row down
+    // product, otherwise its bf16 terms
+    const bool down_rows = few_rows(T, F, H, yf, L.down);
+    if (yf && down_rows) eg.h_terms = 0;
+    if (few_rows(T, H, 2 * (int64_t)F, xf, L.gu)) {
         const DenseRowsParams G{x, (const uint16_t *)w->gate, (const uint16_t *)w->up, eg, T, F, H, xf};
         if (dense_rows_gated_launch(G, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    } else {
+        DenseParams P;
+        memset(&P, 0, sizeof(P));
+        if ((rc = x_segments(P, x, xf, T, H, (uint16_t *)at(ws, L.x3), st))) return rc;
+        for (int i = 0; i < P.nseg; ++i) {
+            P.seg[i].b = (const uint16_t *)w->gate;
+            P.seg[i].b2 = (const uint16_t *)w->up;
+            P.seg[i].ldb = H;
+        }
+        set_plan(P, L.gu, T, F, (int)(ksteps(H) * P.nseg), (float *)at(ws, L.part));
+        P.e = eg;
+        if (dense_gated_launch(P, L.gu.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    }
+    if (down_rows) {
         const DenseRowsParams D{h, (const uint16_t *)w->down, nullptr, ed, T, H, F, yf};
         return launch_err(dense_rows_linear_launch(D, st));
     }
-    DenseParams P;
-    memset(&P, 0, sizeof(P));
-    if ((rc = x_segments(P, x, xf, T, H, (uint16_t *)at(ws, L.x3), st))) return rc;
-    for (int i = 0; i < P.nseg; ++i) {
-        P.seg[i].b = (const uint16_t *)w->gate;
-        P.seg[i].b2 = (const uint16_t *)w->up;
-        P.seg[i].ldb = H;
-    }
-    set_plan(P, L.gu, T, F, (int)(ksteps(H) * P.nseg), (float *)at(ws, L.part));
-    P.e = eg;
-    if (dense_gated_launch(P, L.gu.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
     DenseParams D;
     memset(&D, 0, sizeof(D));
     D.nseg = yf ? 3 : 1;
@@ -415,42 +511,38 @@ int moe_gated_ffn_backward(const void *dy, const void *x, int32_t T, const moe_d
         P.e.h = ddown ? h : nullptr;
         if (dense_dgated_launch(P, L.dh.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
-    if (dx && T != 0) {  // dx = dg Wg + du Wu
-        DenseParams P;
-        memset(&P, 0, sizeof(P));
-        P.nseg = 2;
-        P.seg[0] = DenseSeg{dgu, (const uint16_t *)w->gate, nullptr, 2 * (int64_t)F, H, F};
-        P.seg[1] = DenseSeg{dgu + F, (const uint16_t *)w->up, nullptr, 2 * (int64_t)F, H, F};
-        set_plan(P, L.dx, T, H, (int)(2 * ksteps(F)), part);
-        P.e.y = dx;
-        if (dense_dx_launch(P, L.dx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    DenseParams X, W[2], *dws[2];
+    memset(&X, 0, sizeof(X));
+    memset(W, 0, sizeof(W));
+    Plan pdw[2];
+    int n = 0;
+    const bool with_dx = dx && T != 0;
+    if (with_dx) {  // dx = dg Wg + du Wu
+        X.nseg = 2;
+        X.seg[0] = DenseSeg{dgu, (const uint16_t *)w->gate, nullptr, 2 * (int64_t)F, H, F};
+        X.seg[1] = DenseSeg{dgu + F, (const uint16_t *)w->up, nullptr, 2 * (int64_t)F, H, F};
+        set_plan(X, L.dx, T, H, (int)(2 * ksteps(F)), part);
+        X.e.y = dx;
     }
-    if (dgate || dup) {  // [dg du]^T x
-        DenseParams P;
-        memset(&P, 0, sizeof(P));
+    auto grad = [&](const DenseSeg &g, const Plan &p, int M, int N, void *y, void *y2, int m_split) {
+        DenseParams &P = W[n];
         P.nseg = 1;
-        P.seg[0] = DenseSeg{dgu, (const uint16_t *)x, nullptr, 2 * (int64_t)F, H, T};
-        set_plan(P, L.dw, 2 * F, H, (int)ksteps(T), part);
-        P.e.y = dgate;
-        P.e.y2 = dup;
-        P.e.m_split = F;
+        P.seg[0] = g;
+        set_plan(P, p, M, N, (int)ksteps(T), part);
+        P.e.y = y;
+        P.e.y2 = y2;
+        P.e.m_split = m_split;
         P.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
         P.e.accumulate = accumulate != 0;
-        if (dense_dw_launch(P, L.dw.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
-    }
-    if (ddown) {  // dy^T h
-        DenseParams P;
-        memset(&P, 0, sizeof(P));
-        P.nseg = 1;
-        P.seg[0] = DenseSeg{(const uint16_t *)dy, h, nullptr, H, F, T};
-        set_plan(P, L.dd, H, F, (int)ksteps(T), part);
-        P.e.y = ddown;
-        P.e.m_split = H;
-        P.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
-        P.e.accumulate = accumulate != 0;
-        if (dense_dw_launch(P, L.dd.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
-    }
-    return MOE_OK;
+        pdw[n] = p;
+        dws[n] = &P;
+        ++n;
+    };
+    if (dgate || dup)  // [dg du]^T x
+        grad(DenseSeg{dgu, (const uint16_t *)x, nullptr, 2 * (int64_t)F, H, T}, L.dw, 2 * F, H, dgate, dup, F);
+    if (ddown)  // dy^T h
+        grad(DenseSeg{(const uint16_t *)dy, h, nullptr, H, F, T}, L.dd, H, F, ddown, nullptr, H);
+    return launch_grads(with_dx ? &X : nullptr, L.dx, dws, pdw, n, st);
 }
 
 }  // extern "C"

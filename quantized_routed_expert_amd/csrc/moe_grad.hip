@@ -1,5 +1,6 @@
 // moe_grad.hip -- the dense backward passes' plain products: the input
-// gradient (C = A B) and the weight gradients (C = A^T B).
+// gradient (C = A B) and the weight gradients (C = A^T B), each alone or all in
+// one launch.
 #include "moe_dense.h"
 
 namespace moe {
@@ -9,6 +10,13 @@ hipError_t dense_dx_launch(const DenseParams &P, int tile, hipStream_t st) {
 }
 hipError_t dense_dw_launch(const DenseParams &P, int tile, hipStream_t st) {
     return dense_launch_t<DN_TN, DN_EPI_GRAD>(P, tile, st);
+}
+hipError_t dense_grads_launch(const DenseGradsParams &A, int tile, hipStream_t st) {
+    const dim3 grid((unsigned)(A.tiles[0] + A.tiles[1] + A.tiles[2]));
+#define DN_LAUNCH(THREADS, ...) hipLaunchKernelGGL((k_dense_grads<__VA_ARGS__>), grid, dim3(THREADS), 0, st, A)
+    DN_TILE_SWITCH(tile, DN_LAUNCH)
+#undef DN_LAUNCH
+    return hipGetLastError();
 }
 
 }  // namespace moe

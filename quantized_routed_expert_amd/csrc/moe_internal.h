@@ -315,6 +315,13 @@ struct DenseParams {
     int splits, steps_per_split;
 };
 
+// The products of a backward pass that run side by side: which[i] is 0 (dx)
+// or 1 + the index of a weight gradient, tiles[i] its tiles.
+struct DenseGradsParams {
+    DenseParams dx, dw[2];
+    int which[3], tiles[3];
+};
+
 // Few rows (a decode window): C = A B^T by streaming B once, k split over
 // waves; A in bf16 or fp32.
 constexpr int DN_ROWS_MAX = 64;
