@@ -77,8 +77,51 @@ constexpr int CUS = 256;  // (workspace sizes do not depend on the device at han
 double tile_us(const TileCost &c, int64_t steps) { return c.fixed + c.step * (double)ceil_div(steps, c.groups); }
 double out_us(int64_t M, int64_t N) { return (double)M * (double)N * 2e-6 * US_PER_MB; }
 
+// Time until the last of k sections of tiles (n[i] tiles of us[i] each, started
+// in order) is done, each CU taking the next tile when it is free.
+double tiles_us(const double *us, const int64_t *n, int k) {
+    struct {
+        double at;
+        int64_t cus;
+    } q[16] = {{0.0, CUS}};  // CUs by the time they are free at
+    int nq = 1;
+    for (int i = 0; i < k; ++i) {
+        int64_t left = n[i];
+        if (left > 4 * CUS) {  // whole rounds at once
+            const int64_t rounds = left / CUS - 2;
+            for (int j = 0; j < nq; ++j) q[j].at += (double)rounds * us[i];
+            left -= rounds * CUS;
+        }
+        while (left > 0) {
+            int a = 0, b = -1;
+            for (int j = 1; j < nq; ++j)
+                if (q[j].at < q[a].at) a = j;
+            const int64_t take = q[a].cus < left ? q[a].cus : left;
+            const double done = q[a].at + us[i];
+            left -= take;
+            q[a].cus -= take;
+            for (int j = 0; j < nq; ++j)
+                if (j != a && (q[j].at == done || (nq == 16 && b < 0))) b = j;
+            if (b >= 0) {
+                q[b].cus += take;
+                q[b].at = q[b].at > done ? q[b].at : done;
+                if (q[a].cus == 0) q[a] = q[--nq];
+            } else if (q[a].cus == 0) {
+                q[a].at = done;
+                q[a].cus = take;
+            } else {
+                q[nq].at = done;
+                q[nq++].cus = take;
+            }
+        }
+    }
+    double last = 0.0;
+    for (int j = 0; j < nq; ++j) last = q[j].at > last ? q[j].at : last;
+    return last;
+}
+
 #ifdef DN_FORCE
-int g_force_tile = -1, g_force_split = 1, g_force_rows = -1;
+int g_force_tile = -1, g_force_split = 1, g_force_rows = -1, g_force_merge = -1;
 #endif
 // C of M x N columns of the weight side (gated: 2F) over `steps` 64-k steps
 Plan make_plan(int64_t M, int64_t N, int64_t steps) {
@@ -218,33 +261,7 @@ int launch_grads(const DenseParams *dx, const Plan &pdx, DenseParams *const *dw,
         which[k++] = 1 + i;
         apart += pdw[i].us;
     }
-    // together: the tiles' times over the CUs, and half a tile for the last round
-    int best = -1;
-    double best_us = 1e30;
-    for (int t = 0; t < DN_TILES; ++t) {
-        const TileCost &c = TILES[t];
-        double sum = 0.0, out = 0.0, least = 1e30;
-        for (int i = 0; i < k; ++i) {
-            const double us = tile_us(c, all[i]->steps);
-            sum += us * (double)(ceil_div(all[i]->M, c.bm) * ceil_div(all[i]->N, c.bn));
-            out += out_us(all[i]->M, all[i]->N);
-            least = us < least ? us : least;
-        }
-        const double us = US_LAUNCH + out + (sum / CUS < least ? least : sum / CUS + 0.5 * least);
-        if (us < best_us) {
-            best_us = us;
-            best = t;
-        }
-    }
-    if (k < 2 || apart <= best_us) {
-        if (dx && dense_dx_launch(*dx, pdx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
-        for (int i = 0; i < n; ++i)
-            if (dense_dw_launch(*dw[i], pdw[i].tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
-        return MOE_OK;
-    }
-    DenseGradsParams A;
-    memset(&A, 0, sizeof(A));
-    for (int i = 0; i < k; ++i) {  // longest tiles first
+    for (int i = 1; i < k; ++i) {  // longest tiles first
         for (int j = i; j > 0 && all[j]->steps > all[j - 1]->steps; --j) {
             const DenseParams *p = all[j];
             const int w = which[j];
@@ -254,6 +271,35 @@ int launch_grads(const DenseParams *dx, const Plan &pdx, DenseParams *const *dw,
             which[j - 1] = w;
         }
     }
+    int best = -1;
+    double best_us = 1e30;
+    for (int t = 0; t < DN_TILES; ++t) {
+        const TileCost &c = TILES[t];
+        double us[3], out = 0.0;
+        int64_t tiles[3];
+        for (int i = 0; i < k; ++i) {
+            us[i] = tile_us(c, all[i]->steps);
+            tiles[i] = ceil_div(all[i]->M, c.bm) * ceil_div(all[i]->N, c.bn);
+            out += out_us(all[i]->M, all[i]->N);
+        }
+        const double all_us = US_LAUNCH + out + tiles_us(us, tiles, k);
+        if (all_us < best_us) {
+            best_us = all_us;
+            best = t;
+        }
+    }
+#ifdef DN_FORCE
+    if (g_force_merge == 9) best_us = 1e30;
+    if (g_force_merge >= 0 && g_force_merge < 9) { best = g_force_merge; best_us = 0; }
+#endif
+    if (k < 2 || apart <= best_us) {
+        if (dx && dense_dx_launch(*dx, pdx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+        for (int i = 0; i < n; ++i)
+            if (dense_dw_launch(*dw[i], pdw[i].tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+        return MOE_OK;
+    }
+    DenseGradsParams A;
+    memset(&A, 0, sizeof(A));
     const TileCost &c = TILES[best];
     for (int i = 0; i < k; ++i) {
         DenseParams &P = which[i] == 0 ? A.dx : A.dw[which[i] - 1];
@@ -286,6 +332,7 @@ int x_segments(DenseParams &P, const void *x, bool x_f32, int64_t T, int64_t K, 
 extern "C" {
 #ifdef DN_FORCE
 void dn_force_rows(int r) { g_force_rows = r; }
+void dn_force_merge(int r) { g_force_merge = r; }
 void dn_force(int tile, int split) { g_force_tile = tile; g_force_split = split; }
 #endif
 
