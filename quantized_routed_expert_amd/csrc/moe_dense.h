@@ -186,6 +186,40 @@ __device__ __forceinline__ void dn_act(int act, float (&v)[V]) {
 }
 
 // ---------------------------------------------------------------------------
+// Sums handed from workgroup to workgroup: device-scope accesses (they bypass
+// the caches that XCDs do not share), counted on a counter that is zero
+// between calls.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void dn_store_dev(float4v *p, float4v v) {
+    uint64_t q[2];
+    __builtin_memcpy(q, &v, 16);
+    __hip_atomic_store((uint64_t *)p, q[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store((uint64_t *)p + 1, q[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float4v dn_load_dev(const float4v *p) {
+    uint64_t q[2];
+    q[0] = __hip_atomic_load((const uint64_t *)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    q[1] = __hip_atomic_load((const uint64_t *)p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    float4v v;
+    __builtin_memcpy(&v, q, 16);
+    return v;
+}
+// After a workgroup's dn_store_dev: whether it is the last of n (all threads
+// get the answer; the last sets the counter back to zero).  s_last: LDS.
+__device__ __forceinline__ bool dn_last(uint32_t *counter, uint32_t n, uint32_t *s_last) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
+    __builtin_amdgcn_s_waitcnt(0);  // this wave's stores have arrived
+    __syncthreads();                // every wave's have
+    if (threadIdx.x == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *s_last = before == n - 1;
+        if (before == n - 1) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    return *s_last != 0;
+}
+
+// ---------------------------------------------------------------------------
 // Epilogues: V consecutive columns from n on of row m
 // ---------------------------------------------------------------------------
 // z = v + bias (kept in bf16 if asked); y = act(z) + residual
@@ -599,10 +633,10 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
     wait_vm<0>();  // (the last loads: their LDS is released when the workgroup ends)
 
     // Results in units: (row block i, pair of column blocks).  With groups,
-    // unit u belongs to group u % KG, which adds the others' sums from LDS.
+    // unit u belongs to group u % KG, which adds the groups' sums from LDS.
     // A unit's two column blocks are j, j + 1; gated: the gate blocks j, j + 2
     // (with the up blocks after them), or one gate block where a wave has one.
-    constexpr int JP = GATED && NS == 2 ? 1 : 2, UJ = NS / (GATED ? 2 * JP : JP);
+    constexpr int JP = GATED && NS == 2 ? 1 : 2, UJ = NS / (GATED ? 2 * JP : JP), UB = NS / UJ;  // UB: blocks of a unit
     typedef float4v LdsSums[KG][NW][MS * NS][64];
     if constexpr (KG > 1) {
         __syncthreads();
@@ -612,6 +646,56 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
 #pragma unroll
             for (int j = 0; j < NS; ++j) sums[grp][wave][i * NS + j][lane] = acc[i][j];
         __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MS; ++i)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                if ((i * UJ + j / UB) % KG != grp) continue;
+                float4v v = sums[0][wave][i * NS + j][lane];
+#pragma unroll
+                for (int g = 1; g < KG; ++g) v += sums[g][wave][i * NS + j][lane];
+                acc[i][j] = v;
+            }
+    }
+    // Split: each workgroup leaves its tile's sums, lane by lane; the last one
+    // of the tile adds them in the splits' order.
+    if (P.splits > 1) {
+        float4v *const parts = (float4v *)P.part + (int64_t)tile * P.splits * (BM * BN / 4) + wave * (MS * NS * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < MS; ++i)
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                if (KG > 1 && (i * UJ + j / UB) % KG != grp) continue;
+                dn_store_dev(parts + (int64_t)split * (BM * BN / 4) + (i * NS + j) * 64, acc[i][j]);
+            }
+        if (!dn_last(P.counters + (int64_t)tile * DEC_CSTRIDE, (uint32_t)P.splits, (uint32_t *)(smem + DN_LDS<BM, BN, KG> - 16)))
+            return;
+#pragma unroll
+        for (int i = 0; i < MS; ++i)
+#pragma unroll
+            for (int uj = 0; uj < UJ; ++uj) {
+                if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
+                float4v v[UB];
+#pragma unroll
+                for (int j = 0; j < UB; ++j) v[j] = float4v{0.f, 0.f, 0.f, 0.f};
+                constexpr int Q = 4;  // splits' sums in flight
+                for (int q = 0; q < P.splits; q += Q) {
+                    float4v w[Q][UB];
+#pragma unroll
+                    for (int a = 0; a < Q; ++a)
+#pragma unroll
+                        for (int j = 0; j < UB; ++j)
+                            w[a][j] = dn_load_dev(parts + (int64_t)min(q + a, P.splits - 1) * (BM * BN / 4) + (i * NS + uj * UB + j) * 64);
+#pragma unroll
+                    for (int a = 0; a < Q; ++a)
+                        if (q + a < P.splits) {
+#pragma unroll
+                            for (int j = 0; j < UB; ++j) v[j] += w[a][j];
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < UB; ++j) acc[i][uj * UB + j] = v[j];
+            }
     }
 #pragma unroll
     for (int i = 0; i < MS; ++i) {
@@ -619,37 +703,16 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
 #pragma unroll
         for (int uj = 0; uj < UJ; ++uj) {
             if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
-            // the unit's sums, block by block
-            auto block = [&](int j) {
-                float4v v = acc[i][j];
-                if constexpr (KG > 1) {
-                    LdsSums &sums = *(LdsSums *)smem;
-                    v = sums[0][wave][i * NS + j][lane];
-#pragma unroll
-                    for (int g = 1; g < KG; ++g) v += sums[g][wave][i * NS + j][lane];
-                }
-                return v;
-            };
             if constexpr (GATED) {
                 const int j0 = uj * 2 * JP;
                 const int nb = (int)n0 + (b_row >> 1) + 16 * JP * uj;  // first column of the unit
                 float4v g[JP], u[JP];
 #pragma unroll
                 for (int p = 0; p < JP; ++p) {
-                    g[p] = block(j0 + 2 * p);
-                    u[p] = block(j0 + 2 * p + 1);
+                    g[p] = acc[i][j0 + 2 * p];
+                    u[p] = acc[i][j0 + 2 * p + 1];
                 }
-                if (P.splits > 1) {
-                    float *const part = P.part + ((int64_t)split * P.M + m) * (2 * (int64_t)P.N);
-#pragma unroll
-                    for (int p = 0; p < JP; ++p) {
-                        const int n = nb + 16 * p + 4 * lg;
-                        if (m < P.M && n < P.N) {
-                            *(float4v *)(part + n) = g[p];
-                            *(float4v *)(part + P.N + n) = u[p];
-                        }
-                    }
-                } else if constexpr (JP == 2) {
+                if constexpr (JP == 2) {
                     float gv[8], uv[8];
                     dn_join(g[0], g[1], gv);
                     dn_join(u[0], u[1], uv);
@@ -662,13 +725,8 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
                 }
             } else {
                 const int nb = (int)n0 + b_row + 32 * uj;
-                const float4v v0 = block(2 * uj), v1 = block(2 * uj + 1);
-                if (P.splits > 1) {
-                    float *const part = P.part + ((int64_t)split * P.M + m) * P.N;
-                    const int n = nb + 4 * lg;
-                    if (m < P.M && n < P.N) *(float4v *)(part + n) = v0;
-                    if (m < P.M && n + 16 < P.N) *(float4v *)(part + n + 16) = v1;
-                } else if ((EPI == DN_EPI_LINEAR || EPI == DN_EPI_GRAD) && P.e.y_f32) {
+                const float4v v0 = acc[i][2 * uj], v1 = acc[i][2 * uj + 1];
+                if ((EPI == DN_EPI_LINEAR || EPI == DN_EPI_GRAD) && P.e.y_f32) {
                     // fp32 results: four columns are 16 bytes, a row's four lanes 64
                     const int n = nb + 4 * lg;
                     float a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
@@ -711,38 +769,6 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense_grads
 #endif
 }
 
-// The sum of a split product's parts, in their order, and the epilogue.
-template <int EPI>
-__global__ __launch_bounds__(256) void k_dense_join(DenseParams P) {
-    const int64_t per = P.N / 8, total = per * P.M;
-    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
-        const int64_t m = q / per;
-        const int n = (int)(q - m * per) * 8;
-        constexpr bool GATED = EPI == DN_EPI_GATED;
-        const int64_t ld = GATED ? 2 * (int64_t)P.N : P.N;
-        const float *p = P.part + m * ld + n;
-        float v[8], u[8];
-        dn_load_f32<8>(p, v);
-        if constexpr (GATED) dn_load_f32<8>(p + P.N, u);
-        for (int s = 1; s < P.splits; ++s) {
-            float w[8];
-            p += (int64_t)P.M * ld;
-            dn_load_f32<8>(p, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += w[i];
-            if constexpr (GATED) {
-                dn_load_f32<8>(p + P.N, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] += w[i];
-            }
-        }
-        if constexpr (GATED)
-            dn_epi_gated<8, DN_ACT_ANY>(P.e, P.M, P.N, m, n, v, u);
-        else
-            dn_epi<EPI, 8, DN_ACT_ANY>(P, m, n, v);
-    }
-}
-
 // launch(tile shape...) for a tile
 #define DN_TILE_SWITCH(tile, LAUNCH)                             \
     switch (tile) {                                              \
@@ -753,7 +779,7 @@ __global__ __launch_bounds__(256) void k_dense_join(DenseParams P) {
         default: return hipErrorInvalidValue;                    \
     }
 
-// One product of the given form and epilogue, and its join when it is split.
+// One product of the given form and epilogue.
 template <int FORM, int EPI, int ACT>
 hipError_t dense_tile_t(const DenseParams &P, int tile, hipStream_t st) {
     const dim3 grid((unsigned)(P.tiles_m * P.tiles_n), (unsigned)P.splits);
@@ -764,20 +790,14 @@ hipError_t dense_tile_t(const DenseParams &P, int tile, hipStream_t st) {
 }
 template <int FORM, int EPI>
 hipError_t dense_launch_t(const DenseParams &P, int tile, hipStream_t st) {
-    hipError_t e;
     constexpr bool A = EPI != DN_EPI_GRAD && !(FORM == DN_NN && EPI == DN_EPI_LINEAR);  // with an activation
-    switch (A && P.splits == 1 ? P.e.act : DN_ACT_NONE) {
-        case DN_ACT_SILU: e = dense_tile_t<FORM, EPI, A ? DN_ACT_SILU : 0>(P, tile, st); break;
-        case DN_ACT_GELU: e = dense_tile_t<FORM, EPI, A ? DN_ACT_GELU : 0>(P, tile, st); break;
-        case DN_ACT_GELU_TANH: e = dense_tile_t<FORM, EPI, A ? DN_ACT_GELU_TANH : 0>(P, tile, st); break;
-        case DN_ACT_RELU: e = dense_tile_t<FORM, EPI, A ? DN_ACT_RELU : 0>(P, tile, st); break;
-        default: e = dense_tile_t<FORM, EPI, DN_ACT_NONE>(P, tile, st); break;
+    switch (A ? P.e.act : DN_ACT_NONE) {
+        case DN_ACT_SILU: return dense_tile_t<FORM, EPI, A ? DN_ACT_SILU : 0>(P, tile, st);
+        case DN_ACT_GELU: return dense_tile_t<FORM, EPI, A ? DN_ACT_GELU : 0>(P, tile, st);
+        case DN_ACT_GELU_TANH: return dense_tile_t<FORM, EPI, A ? DN_ACT_GELU_TANH : 0>(P, tile, st);
+        case DN_ACT_RELU: return dense_tile_t<FORM, EPI, A ? DN_ACT_RELU : 0>(P, tile, st);
+        default: return dense_tile_t<FORM, EPI, DN_ACT_NONE>(P, tile, st);
     }
-    if (e != hipSuccess || P.splits == 1) return e;
-    const int64_t work = (int64_t)P.M * (P.N / 8);
-    const int64_t blocks = (work + 255) / 256;
-    hipLaunchKernelGGL((k_dense_join<EPI>), dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, st, P);
-    return hipGetLastError();
 }
 
 }  // namespace moe

@@ -59,19 +59,19 @@ struct Plan {
 };
 // The least estimated time over the tiles and split counts.  Rounds of one
 // tile per CU; a tile takes a fixed time and one per step (of its longest
-// group), the results one per MB, a split the joining launch and the parts'
-// traffic.  Fitted to 380 launches of 51 products (64 x 2048 x 2048 to
-// 8192 x 4096 x 11008, each tile, splits of 1 to 8; 9% off in the mean; the
-// choice costs 0.5% over the best of each): e.g. 2048 x 2048 outputs over 512 k
-// take 10 us in 128 x 128 tiles and 20 in 64 x 64, 2048 x 512 outputs over
-// 2048 k 18 and 10.
+// group), the results one per MB, a split the hand-over and the parts'
+// traffic.  Fitted to the launches of 57 products (16 x 2048 x 768 to
+// 8192 x 4096 x 11008, each tile, splits of 1 to 16) that are within 1.9 times
+// the best of their product: 11% off in the mean, and the choice costs 1% over
+// the best.  E.g. 2048 x 2048 outputs over 512 k take 10 us in 128 x 128 tiles
+// and 20 in 64 x 64; 2048 x 512 outputs over 2048 k 17 and 10.
 struct TileCost {
     int bm, bn, groups;
     double fixed, step;  // us
 };
 constexpr TileCost TILES[DN_TILES] = {
-    {256, 256, 1, 5.1, 1.10}, {256, 128, 1, 2.6, 0.68}, {128, 128, 2, 2.7, 0.78}, {64, 64, 4, 2.3, 0.74}};
-constexpr double US_LAUNCH = 1.5, US_JOIN = 4.9, US_PER_MB = 0.16, US_PER_PART_MB = 0.67;
+    {256, 256, 1, 5.2, 1.22}, {256, 128, 1, 2.9, 0.71}, {128, 128, 2, 3.0, 0.77}, {64, 64, 4, 2.35, 0.74}};
+constexpr double US_LAUNCH = 1.6, US_JOIN = 2.0, US_PER_MB = 0.3, US_PER_PART_MB = 0.82;
 constexpr int CUS = 256;  // (workspace sizes do not depend on the device at hand)
 
 double tile_us(const TileCost &c, int64_t steps) { return c.fixed + c.step * (double)ceil_div(steps, c.groups); }
@@ -134,10 +134,12 @@ Plan make_plan(int64_t M, int64_t N, int64_t steps) {
 #ifdef DN_FORCE
             if (g_force_tile >= 0 && (t != g_force_tile || s != g_force_split)) continue;
 #endif
-            if (s > 1 && (tiles * s * c.bm * c.bn > (int64_t)DN_SPLIT_TILES * 128 * 128 || steps < 4 * s * c.groups)) break;
+            if (s > 1 && (tiles * s * c.bm * c.bn > (int64_t)DN_SPLIT_TILES * 128 * 128 || tiles > WS_COUNTERS ||
+                          steps < 2 * s * c.groups))
+                break;
             const int64_t per = ceil_div(steps, s);
             double us = US_LAUNCH + (double)ceil_div(tiles * s, CUS) * tile_us(c, per) + out_us(M, N);
-            if (s > 1) us += US_JOIN + (double)s * (double)M * (double)N * 4e-6 * US_PER_PART_MB;
+            if (s > 1) us += US_JOIN + (double)(s * tiles * c.bm * c.bn) * 4e-6 * US_PER_PART_MB;
             if (us < best.us) best = Plan{t, (int)tm, (int)tn, (int)ceil_div(steps, per), (int)per, us};
         }
     }
@@ -179,7 +181,7 @@ struct Carve {  // workspace regions after the head
 };
 uint8_t *at(void *ws, int64_t off) { return (uint8_t *)ws + off; }
 
-void set_plan(DenseParams &P, const Plan &p, int M, int N, int steps, float *part) {
+void set_plan(DenseParams &P, const Plan &p, int M, int N, int steps, void *ws, int64_t part) {
     P.M = M;
     P.N = N;
     P.steps = steps;
@@ -187,7 +189,8 @@ void set_plan(DenseParams &P, const Plan &p, int M, int N, int steps, float *par
     P.tiles_n = p.tiles_n;
     P.splits = p.splits;
     P.steps_per_split = p.per;
-    P.part = part;
+    P.part = (float *)at(ws, part);
+    P.counters = (uint32_t *)ws;
 }
 // The parts of a split product: at most DN_SPLIT_TILES tiles of 128 x 128
 // over all splits, whatever the sizes; a fixed region, so that a workspace
@@ -382,7 +385,7 @@ int moe_linear(const void *x, int32_t x_dtype, int32_t T, int32_t in, const void
         P.seg[i].b = (const uint16_t *)w;
         P.seg[i].ldb = in;
     }
-    set_plan(P, L.fwd, T, out, (int)(ksteps(in) * P.nseg), (float *)at(ws, L.part));
+    set_plan(P, L.fwd, T, out, (int)(ksteps(in) * P.nseg), ws, L.part);
     P.e = e;
     return launch_err(dense_linear_launch(P, L.fwd.tile, S(stream)));
 }
@@ -408,6 +411,7 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
     const bool with_act = act != MOE_ACT_NONE;
     const uint16_t *dz = with_act ? (const uint16_t *)at(ws, L.dz) : (const uint16_t *)dy;
     int nchunks = 0;
+    bool summed = false;
     if (T != 0 && (with_act || dbias)) {
         DzParams D;
         memset(&D, 0, sizeof(D));
@@ -421,9 +425,14 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
         // chunks of at least 16 rows, at most DN_DZ_CHUNKS of them
         D.rows_per_chunk = max64(ceil_div(T, DN_DZ_CHUNKS), 16);
         nchunks = D.nchunks = (int)ceil_div(T, D.rows_per_chunk);
+        D.counters = (uint32_t *)ws;
+        D.out = ceil_div(out, 256) <= WS_COUNTERS ? dbias : nullptr;
+        D.out_f32 = dw_dtype == MOE_DTYPE_F32;
+        D.accumulate = accumulate != 0;
+        summed = D.out != nullptr;
         if (dense_dz_launch(D, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
-    if (dbias) {
+    if (dbias && !summed) {
         ColsumParams C{(const float *)at(ws, L.chunks), dbias, out, nchunks, dw_dtype == MOE_DTYPE_F32, accumulate != 0};
         if (dense_colsum_launch(C, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
@@ -434,13 +443,13 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
     if (with_dx) {
         X.nseg = 1;
         X.seg[0] = DenseSeg{dz, (const uint16_t *)w, nullptr, out, in, out};
-        set_plan(X, L.dx, T, in, (int)ksteps(out), (float *)at(ws, L.bpart));
+        set_plan(X, L.dx, T, in, (int)ksteps(out), ws, L.bpart);
         X.e.y = dx;
     }
     if (dw) {
         W.nseg = 1;
         W.seg[0] = DenseSeg{dz, (const uint16_t *)x, nullptr, out, in, T};
-        set_plan(W, L.dw, out, in, (int)ksteps(T), (float *)at(ws, L.bpart));
+        set_plan(W, L.dw, out, in, (int)ksteps(T), ws, L.bpart);
         W.e.y = dw;
         W.e.m_split = out;
         W.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
@@ -506,7 +515,7 @@ int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn
             P.seg[i].b2 = (const uint16_t *)w->up;
             P.seg[i].ldb = H;
         }
-        set_plan(P, L.gu, T, F, (int)(ksteps(H) * P.nseg), (float *)at(ws, L.part));
+        set_plan(P, L.gu, T, F, (int)(ksteps(H) * P.nseg), ws, L.part);
         P.e = eg;
         if (dense_gated_launch(P, L.gu.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
@@ -519,7 +528,7 @@ int moe_gated_ffn(const void *x, int32_t x_dtype, int32_t T, const moe_dense_ffn
     D.nseg = yf ? 3 : 1;
     for (int i = 0; i < D.nseg; ++i)
         D.seg[i] = DenseSeg{h + (int64_t)i * T * F, (const uint16_t *)w->down, nullptr, F, F, F};
-    set_plan(D, L.down, T, H, (int)(ksteps(F) * D.nseg), (float *)at(ws, L.part));
+    set_plan(D, L.down, T, H, (int)(ksteps(F) * D.nseg), ws, L.part);
     D.e = ed;
     return launch_err(dense_linear_launch(D, L.down.tile, st));
 }
@@ -545,13 +554,12 @@ int moe_gated_ffn_backward(const void *dy, const void *x, int32_t T, const moe_d
     if ((rc = device_cus(cus))) return rc;
     const hipStream_t st = S(stream);
     uint16_t *dgu = (uint16_t *)at(ws, L.dgu), *h = (uint16_t *)at(ws, L.bh);
-    float *part = (float *)at(ws, L.bpart);
     if (T != 0) {  // dh = dy Wd, then dg, du and h
         DenseParams P;
         memset(&P, 0, sizeof(P));
         P.nseg = 1;
         P.seg[0] = DenseSeg{(const uint16_t *)dy, (const uint16_t *)w->down, nullptr, H, F, H};
-        set_plan(P, L.dh, T, F, (int)ksteps(H), part);
+        set_plan(P, L.dh, T, F, (int)ksteps(H), ws, L.bpart);
         P.e.act = w->act;
         P.e.gu_in = (const uint16_t *)gu;
         P.e.dgu = dgu;
@@ -568,14 +576,14 @@ int moe_gated_ffn_backward(const void *dy, const void *x, int32_t T, const moe_d
         X.nseg = 2;
         X.seg[0] = DenseSeg{dgu, (const uint16_t *)w->gate, nullptr, 2 * (int64_t)F, H, F};
         X.seg[1] = DenseSeg{dgu + F, (const uint16_t *)w->up, nullptr, 2 * (int64_t)F, H, F};
-        set_plan(X, L.dx, T, H, (int)(2 * ksteps(F)), part);
+        set_plan(X, L.dx, T, H, (int)(2 * ksteps(F)), ws, L.bpart);
         X.e.y = dx;
     }
     auto grad = [&](const DenseSeg &g, const Plan &p, int M, int N, void *y, void *y2, int m_split) {
         DenseParams &P = W[n];
         P.nseg = 1;
         P.seg[0] = g;
-        set_plan(P, p, M, N, (int)ksteps(T), part);
+        set_plan(P, p, M, N, (int)ksteps(T), ws, L.bpart);
         P.e.y = y;
         P.e.y2 = y2;
         P.e.m_split = m_split;

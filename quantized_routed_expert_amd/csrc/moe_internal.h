@@ -267,7 +267,8 @@ struct PrepareParams {
 
 // Head of every workspace: after the slot and slice counters the error word
 // (a line of its own), then the per-workgroup epochs.
-constexpr size_t COUNTER_WORDS = (size_t)(2 * DEC_MAX_SLOTS + DEC_MAX_SLICES + 1) * DEC_CSTRIDE + EPOCH_SLOTS;
+constexpr int WS_COUNTERS = 2 * DEC_MAX_SLOTS + DEC_MAX_SLICES;  // zero between calls of any kind
+constexpr size_t COUNTER_WORDS = (size_t)(WS_COUNTERS + 1) * DEC_CSTRIDE + EPOCH_SLOTS;
 
 // The current device's compute units (a MOE_* status).
 int device_cus(int &cus);
@@ -308,7 +309,8 @@ struct DenseEpi {
 struct DenseParams {
     DenseSeg seg[DN_MAX_SEG];
     DenseEpi e;
-    float *part;      // split products: [splits][M][N] fp32 (gated: [splits][M][2N])
+    float *part;         // split products: [tile][split] sums of a tile, as its lanes hold them
+    uint32_t *counters;  // ... and one counter per tile, DEC_CSTRIDE words apart (zero between calls)
     int nseg, steps;  // 64-k steps over all products of the sum
     int M, N;         // output rows and columns (gated: N = F)
     int tiles_m, tiles_n;
@@ -343,8 +345,10 @@ struct DzParams {
     const uint16_t *dy, *z;  // [T][N]; z null: no activation
     uint16_t *dz;            // [T][N] or null
     float *part;             // [nchunks][N] or null
+    uint32_t *counters;      // one per 256 columns, DEC_CSTRIDE words apart (zero between calls)
+    void *out;               // [N] the sums, or null: by k_dense_colsum
     int64_t rows_per_chunk;
-    int T, N, nchunks, act;
+    int T, N, nchunks, act, out_f32, accumulate;
 };
 struct ColsumParams {
     const float *part;  // [nchunks][N]

@@ -16,6 +16,17 @@ __global__ __launch_bounds__(256) void k_dense_split3(const float *x, uint16_t *
     }
 }
 
+__device__ __forceinline__ void dn_store_sum(void *out, int c, float v, int out_f32, int accumulate) {
+    if (out_f32) {
+        float *o = (float *)out + c;
+        *o = accumulate ? *o + v : v;
+    } else {
+        uint16_t *o = (uint16_t *)out + c;
+        if (accumulate) v += dn_bf(*o);
+        *o = (uint16_t)(dn_pack(v, 0.f) & 0xFFFFu);
+    }
+}
+
 // dz = dy act'(z) for 256 columns (32 threads of 8) and one chunk of rows (8
 // at a time), and the chunk's column sums (from the unrounded values: eight
 // row lanes in fp32, then joined in order).  Bound by its reads and writes.
@@ -55,11 +66,23 @@ __global__ __launch_bounds__(256) void k_dense_dz(DzParams P) {
         float v = s_sum[0][tid];
 #pragma unroll
         for (int i = 1; i < 8; ++i) v += s_sum[i][tid];
-        P.part[(int64_t)blockIdx.y * P.N + c] = v;
+        if (P.out)
+            __hip_atomic_store(&P.part[(int64_t)blockIdx.y * P.N + c], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else
+            P.part[(int64_t)blockIdx.y * P.N + c] = v;
     }
+    // the last workgroup of these columns adds the chunks, in order
+    __shared__ uint32_t s_last;
+    if (!P.out || !dn_last(P.counters + (int64_t)blockIdx.x * DEC_CSTRIDE, (uint32_t)P.nchunks, &s_last) || c >= P.N) return;
+    float v = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < P.nchunks; ++i)
+        v += __hip_atomic_load(&P.part[(int64_t)i * P.N + c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    dn_store_sum(P.out, c, v, P.out_f32, P.accumulate);
 }
 
-// bias gradient: the chunks' sums.  32 columns a workgroup; eight chunk lanes
+// bias gradient where k_dense_dz does not finish it (no rows, or more columns
+// than counters): the chunks' sums.  32 columns a workgroup; eight chunk lanes
 // add every eighth chunk, then are joined in order (nchunks 0: zero).
 __global__ __launch_bounds__(256) void k_dense_colsum(ColsumParams P) {
     __shared__ float s_sum[8][33];
@@ -75,14 +98,7 @@ __global__ __launch_bounds__(256) void k_dense_colsum(ColsumParams P) {
     if (l > 0 || c >= P.N) return;
 #pragma unroll
     for (int i = 1; i < 8; ++i) v += s_sum[i][cl];
-    if (P.out_f32) {
-        float *o = (float *)P.out + c;
-        *o = P.accumulate ? *o + v : v;
-    } else {
-        uint16_t *o = (uint16_t *)P.out + c;
-        if (P.accumulate) v += dn_bf(*o);
-        *o = (uint16_t)(dn_pack(v, 0.f) & 0xFFFFu);
-    }
+    dn_store_sum(P.out, c, v, P.out_f32, P.accumulate);
 }
 
 hipError_t dense_split3_launch(const float *x, uint16_t *out, int64_t n, hipStream_t st) {
