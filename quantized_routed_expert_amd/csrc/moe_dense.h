@@ -220,33 +220,73 @@ __device__ __forceinline__ bool dn_last(uint32_t *counter, uint32_t n, uint32_t 
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues: V consecutive columns from n on of row m
+// Epilogues: V consecutive columns from n on of row m.  What an epilogue reads
+// at its place (DnIn: a residual, kept gate and up, a gradient to add to) is
+// loaded apart, so that a tile's loads can go out ahead of their use.
 // ---------------------------------------------------------------------------
+struct DnIn {
+    u32x4 a, b;
+};
+// raw values: V = 4 takes 8 (bf16) or 16 bytes, V = 8 16 or 32
+template <int V>
+__device__ __forceinline__ void dn_raw(const void *p, int64_t at, bool f32, DnIn &in) {
+    if (f32) {
+        in.a = *(const u32x4 *)((const float *)p + at);
+        if constexpr (V == 8) in.b = *(const u32x4 *)((const float *)p + at + 4);
+    } else if constexpr (V == 8) {
+        in.a = *(const u32x4 *)((const uint16_t *)p + at);
+    } else {
+        const u32x2 q = *(const u32x2 *)((const uint16_t *)p + at);
+        in.a.x = q.x;
+        in.a.y = q.y;
+    }
+}
+// two bf16 in each of V / 2 words
+template <int V>
+__device__ __forceinline__ void dn_unpack(u32x4 q, float (&v)[V]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        v[2 * i] = dn_bf(w[i] & 0xFFFFu);
+        v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+    }
+}
+template <int V>
+__device__ __forceinline__ void dn_add_raw(const DnIn &in, bool f32, float (&v)[V]) {
+    if (f32) {
+        const uint32_t w[8] = {in.a.x, in.a.y, in.a.z, in.a.w, in.b.x, in.b.y, in.b.z, in.b.w};
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += __builtin_bit_cast(float, w[i]);
+    } else {
+        float r[V];
+        dn_unpack<V>(in.a, r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += r[i];
+    }
+}
+template <int V>
+__device__ __forceinline__ void dn_store(void *p, int64_t at, bool f32, const float (&v)[V]) {
+    if (f32)
+        dn_store_f32<V>((float *)p + at, v);
+    else
+        dn_store_bf<V>((uint16_t *)p + at, v);
+}
+
 // z = v + bias (kept in bf16 if asked); y = act(z) + residual
 template <int V, int ACT>
-__device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
+__device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V], const DnIn &in,
+                                              u32x4 bias) {
     const int64_t at = m * N + n;
     if (e.bias) {
         float b[V];
-        dn_load_bf<V>(e.bias + n, b);
+        dn_unpack<V>(bias, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += b[i];
     }
     if (e.z) dn_store_bf<V>(e.z + at, v);
     if (dn_act_of<ACT>(e) != DN_ACT_NONE) dn_act<V>(dn_act_of<ACT>(e), v);
-    if (e.res) {
-        float r[V];
-        if (e.res_f32)
-            dn_load_f32<V>((const float *)e.res + at, r);
-        else
-            dn_load_bf<V>((const uint16_t *)e.res + at, r);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += r[i];
-    }
-    if (e.y_f32)
-        dn_store_f32<V>((float *)e.y + at, v);
-    else
-        dn_store_bf<V>((uint16_t *)e.y + at, v);
+    if (e.res) dn_add_raw<V>(in, e.res_f32, v);
+    dn_store<V>(e.y, at, e.y_f32, v);
 }
 // h = act(g) u.  h enters the down product in bf16; with h_terms = 3 (an fp32
 // y) as three exact bf16 terms, so that y is as good as its type.  g and u
@@ -271,11 +311,11 @@ __device__ __forceinline__ void dn_epi_gated(const DenseEpi &e, int64_t M, int N
 // v = dh: h = act(g) u, dg = dh u act'(g), du = dh act(g), each rounded once
 // to bf16, the type their products take
 template <int V, int ACT>
-__device__ __forceinline__ void dn_epi_dgated(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
+__device__ __forceinline__ void dn_epi_dgated(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V], const DnIn &in) {
     float g[V], u[V], h[V], dg[V], du[V];
     const int64_t at = m * (2 * (int64_t)N) + n;
-    dn_load_bf<V>(e.gu_in + at, g);
-    dn_load_bf<V>(e.gu_in + at + N, u);
+    dn_unpack<V>(in.a, g);
+    dn_unpack<V>(in.b, u);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         float d;
@@ -288,35 +328,39 @@ __device__ __forceinline__ void dn_epi_dgated(const DenseEpi &e, int N, int64_t 
     dn_store_bf<V>(e.dgu + at, dg);
     dn_store_bf<V>(e.dgu + at + N, du);
 }
-// weight gradient: row m of y, or of y2 from m_split on
+// weight gradient: row m of y, or of y2 from m_split on (either may be null);
+// accumulate: on what is there, in its own type
 template <int V>
-__device__ __forceinline__ void dn_epi_grad(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
-    void *y = e.y;
-    if (m >= e.m_split) {
-        y = e.y2;
-        m -= e.m_split;
-    }
+__device__ __forceinline__ void dn_epi_grad(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V], const DnIn &in) {
+    const bool second = m >= e.m_split;
+    void *const y = second ? e.y2 : e.y;
     if (!y) return;
-    const int64_t at = m * N + n;
-    if (e.accumulate) {  // on what is there, in its own type
-        float r[V];
-        if (e.y_f32)
-            dn_load_f32<V>((const float *)y + at, r);
-        else
-            dn_load_bf<V>((const uint16_t *)y + at, r);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += r[i];
+    if (e.accumulate) dn_add_raw<V>(in, e.y_f32, v);
+    dn_store<V>(y, (second ? m - e.m_split : m) * N + n, e.y_f32, v);
+}
+// an epilogue's input, if it has one
+template <int EPI, int V>
+__device__ __forceinline__ void dn_in(const DenseParams &P, int64_t m, int n, DnIn &in) {
+    const DenseEpi &e = P.e;
+    if constexpr (EPI == DN_EPI_LINEAR) {
+        if (e.res) dn_raw<V>(e.res, m * P.N + n, e.res_f32, in);
     }
-    if (e.y_f32)
-        dn_store_f32<V>((float *)y + at, v);
-    else
-        dn_store_bf<V>((uint16_t *)y + at, v);
+    if constexpr (EPI == DN_EPI_DGATED) {
+        const uint16_t *p = e.gu_in + m * (2 * (int64_t)P.N) + n;
+        in.a = *(const u32x4 *)p;
+        in.b = *(const u32x4 *)(p + P.N);
+    }
+    if constexpr (EPI == DN_EPI_GRAD) {
+        const bool second = m >= e.m_split;
+        const void *const y = second ? e.y2 : e.y;
+        if (e.accumulate && y) dn_raw<V>(y, (second ? m - e.m_split : m) * P.N + n, e.y_f32, in);
+    }
 }
 template <int EPI, int V, int ACT>
-__device__ __forceinline__ void dn_epi(const DenseParams &P, int64_t m, int n, float (&v)[V]) {
-    if constexpr (EPI == DN_EPI_LINEAR) dn_epi_linear<V, ACT>(P.e, P.N, m, n, v);
-    if constexpr (EPI == DN_EPI_DGATED) dn_epi_dgated<V, ACT>(P.e, P.N, m, n, v);
-    if constexpr (EPI == DN_EPI_GRAD) dn_epi_grad<V>(P.e, P.N, m, n, v);
+__device__ __forceinline__ void dn_epi(const DenseParams &P, int64_t m, int n, float (&v)[V], const DnIn &in, u32x4 bias) {
+    if constexpr (EPI == DN_EPI_LINEAR) dn_epi_linear<V, ACT>(P.e, P.N, m, n, v, in, bias);
+    if constexpr (EPI == DN_EPI_DGATED) dn_epi_dgated<V, ACT>(P.e, P.N, m, n, v, in);
+    if constexpr (EPI == DN_EPI_GRAD) dn_epi_grad<V>(P.e, P.N, m, n, v, in);
 }
 
 // ---------------------------------------------------------------------------
@@ -401,6 +445,10 @@ __device__ __forceinline__ void dn_tile(const DenseParams &P, int b, int &tm, in
     tm = grp * G + in - tn * rows;
 }
 
+template <int N>
+struct DnInt {
+    static constexpr int value = N;
+};
 struct DnTrue {
     static constexpr bool value = true;
 };
@@ -448,9 +496,9 @@ struct DnCursor {
 
 // Main loop.  A step's 64 k are two halves of 32.  Fragments are double
 // buffered in registers: while the MFMAs of one half run, the other half's
-// fragments are read, so no MFMA waits for LDS.  LDS holds three slices of B
-// and two of A (a slice: one operand, one step).  The first half of step s
-// loads B of s+2 into its third slice, the second half A of s+2 into the one
+// fragments are read, so no MFMA waits for LDS.  LDS holds D slices of A
+// and D + 1 of B (a slice: one operand, one step).  The first half of step s
+// loads B of s+D into its spare slice, the second half A of s+D into the one
 // that A of s has just been read from.  One barrier, in the middle of a step,
 // says both that every wave has read step s and that step s+1 has landed.
 // Loads go out through the whole step: the path into LDS moves 64 bytes a
@@ -462,11 +510,11 @@ struct DnCursor {
 // its own part of the tile's steps; their sums are added in LDS, in order, at
 // the end.  Small tiles spend their time waiting for loads; the groups keep
 // KG times as many in flight and take 1 / KG of the steps.
-template <int BM, int BN, int KG>
-constexpr int DN_LDS = KG * (2 * BM + 3 * BN) * 128;
+template <int BM, int BN, int KG, int D>
+constexpr int DN_LDS = KG * (D * BM + (D + 1) * BN) * 128;
 
 #ifdef __HIP_DEVICE_COMPILE__  // (the host pass needs the kernels' stubs alone: it drops those that use the buffer builtins)
-template <int BM, int BN, int WM, int WN, int KG, int FORM, int EPI, int ACT>
+template <int BM, int BN, int WM, int WN, int KG, int D, int FORM, int EPI, int ACT>
 __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int split, uint8_t *smem) {
     constexpr int NW = WM * WN;  // waves per group
     constexpr bool AKC = FORM != DN_TN, BKC = FORM == DN_NT;
@@ -476,8 +524,8 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
     constexpr int PAIR = GATED ? 16 : 0;  // blocks of 16 gate rows and the same up rows in turn
     typedef DnStream<BM, AKC, NW> SA;
     typedef DnStream<BN, BKC, NW> SB;
-    constexpr int RING = 2 * SA::BYTES + 3 * SB::BYTES;
-    static_assert(RING * KG == DN_LDS<BM, BN, KG>, "slices");
+    constexpr int RING = D * SA::BYTES + (D + 1) * SB::BYTES;
+    static_assert(RING * KG == DN_LDS<BM, BN, KG, D>, "slices");
     static_assert(KG == 1 || BM * BN * 4 <= RING, "the groups' sums fit the slices");
     lds_u8 *const lds_all = (lds_u8 *)smem;
 
@@ -526,7 +574,7 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
     };
     auto a_one = [&](int j) { sa.issue(j, ra, da, wave, pa); };
     auto b_begin = [&](int slice) {
-        db = lds0 + 2 * SA::BYTES + slice * SB::BYTES;
+        db = lds0 + D * SA::BYTES + slice * SB::BYTES;
         pb = sb.past(cb.kleft);
         rb = dn_rsrc(cb.p, cb.range(n0));
         if constexpr (GATED) ru = dn_rsrc(cb.p2, cb.range(n0));
@@ -601,7 +649,7 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
     };
 
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < D; ++t) {
         b_begin(t);
 #pragma unroll
         for (int j = 0; j < SB::NL; ++j) b_one(j);
@@ -611,22 +659,22 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
         for (int j = 0; j < SA::NL; ++j) a_one(j);
         ca.advance(P, m0, rows);
     }
-    wait_vm<SA::NL + SB::NL>();
+    constexpr int NLD = SA::NL + SB::NL;  // loads of a step
+    wait_vm<(D - 1) * NLD>();
     lds_barrier();
-    lds_u8 *const lds_b = lds + 2 * SA::BYTES;
+    lds_u8 *const lds_b = lds + D * SA::BYTES;
 #pragma unroll
     for (int q = 0; q < NF; ++q) read_one(0, lds, lds_b, 0, q);
-    // slices of step s: A's sl_a, B's sl_b
+    // slices of step s: A's sl_a = s % D, B's sl_b = s % (D + 1)
     for (int s = 0, sl_a = 0, sl_b = 0; s < nstep; ++s) {
-        const int nb = sl_b == 2 ? 0 : sl_b + 1;
-        b_begin(nb == 2 ? 0 : nb + 1);
+        b_begin(sl_b == 0 ? D : sl_b - 1);
         half(DnFalse(), 0, lds + sl_a * SA::BYTES, lds_b + sl_b * SB::BYTES, 1);
         cb.advance(P, n0, cols);
         a_begin(sl_a);
-        wait_vm<SB::NL>();
+        wait_vm<(D - 2) * NLD + SB::NL>();  // all but the loads after step s + 1's
         lds_barrier();
-        sl_a ^= 1;
-        sl_b = nb;
+        sl_a = sl_a == D - 1 ? 0 : sl_a + 1;
+        sl_b = sl_b == D ? 0 : sl_b + 1;
         half(DnTrue(), 1, lds + sl_a * SA::BYTES, lds_b + sl_b * SB::BYTES, 0);
         ca.advance(P, m0, rows);
     }
@@ -668,7 +716,7 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
                 if (KG > 1 && (i * UJ + j / UB) % KG != grp) continue;
                 dn_store_dev(parts + (int64_t)split * (BM * BN / 4) + (i * NS + j) * 64, acc[i][j]);
             }
-        if (!dn_last(P.counters + (int64_t)tile * DEC_CSTRIDE, (uint32_t)P.splits, (uint32_t *)(smem + DN_LDS<BM, BN, KG> - 16)))
+        if (!dn_last(P.counters + (int64_t)tile * DEC_CSTRIDE, (uint32_t)P.splits, (uint32_t *)(smem + DN_LDS<BM, BN, KG, D> - 16)))
             return;
 #pragma unroll
         for (int i = 0; i < MS; ++i)
@@ -697,58 +745,101 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
                 for (int j = 0; j < UB; ++j) acc[i][uj * UB + j] = v[j];
             }
     }
+    if constexpr (GATED) {
 #pragma unroll
-    for (int i = 0; i < MS; ++i) {
-        const int64_t m = m0 + a_row + 16 * i + li;
+        for (int i = 0; i < MS; ++i) {
+            const int64_t m = m0 + a_row + 16 * i + li;
 #pragma unroll
-        for (int uj = 0; uj < UJ; ++uj) {
-            if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
-            if constexpr (GATED) {
+            for (int uj = 0; uj < UJ; ++uj) {
+                if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
                 const int j0 = uj * 2 * JP;
                 const int nb = (int)n0 + (b_row >> 1) + 16 * JP * uj;  // first column of the unit
-                float4v g[JP], u[JP];
-#pragma unroll
-                for (int p = 0; p < JP; ++p) {
-                    g[p] = acc[i][j0 + 2 * p];
-                    u[p] = acc[i][j0 + 2 * p + 1];
-                }
                 if constexpr (JP == 2) {
                     float gv[8], uv[8];
-                    dn_join(g[0], g[1], gv);
-                    dn_join(u[0], u[1], uv);
+                    dn_join(acc[i][j0], acc[i][j0 + 2], gv);
+                    dn_join(acc[i][j0 + 1], acc[i][j0 + 3], uv);
                     const int n = nb + dn_joined(lg);
                     if (m < P.M && n < P.N) dn_epi_gated<8, ACT>(P.e, P.M, P.N, m, n, gv, uv);
                 } else {
-                    float gv[4] = {g[0].x, g[0].y, g[0].z, g[0].w}, uv[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+                    const float4v g = acc[i][j0], u = acc[i][j0 + 1];
+                    float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
                     const int n = nb + 4 * lg;
                     if (m < P.M && n < P.N) dn_epi_gated<4, ACT>(P.e, P.M, P.N, m, n, gv, uv);
                 }
-            } else {
-                const int nb = (int)n0 + b_row + 32 * uj;
-                const float4v v0 = acc[i][2 * uj], v1 = acc[i][2 * uj + 1];
-                if ((EPI == DN_EPI_LINEAR || EPI == DN_EPI_GRAD) && P.e.y_f32) {
-                    // fp32 results: four columns are 16 bytes, a row's four lanes 64
-                    const int n = nb + 4 * lg;
-                    float a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
-                    if (m < P.M && n < P.N) dn_epi<EPI, 4, ACT>(P, m, n, a);
-                    if (m < P.M && n + 16 < P.N) dn_epi<EPI, 4, ACT>(P, m, n + 16, b);
-                } else {
-                    float v[8];
-                    dn_join(v0, v1, v);
-                    const int n = nb + dn_joined(lg);
-                    if (m < P.M && n < P.N) dn_epi<EPI, 8, ACT>(P, m, n, v);
-                }
             }
         }
+    } else {
+        // V = 8: a unit's joined blocks (bf16 results); V = 4: fp32 results,
+        // where four columns are 16 bytes and a row's four lanes 64
+        auto finish = [&](auto width) {
+            constexpr int V = decltype(width)::value, SUB = 8 / V;
+            // what row blocks i .. i + PRE - 1 read is in flight while block i
+            // is finished (one at a time, 256 x 256 tiles with an fp32
+            // residual took 30 us longer)
+            constexpr int PRE = MS < 4 ? MS : 4;
+            DnIn in[PRE][UJ][SUB];
+            u32x4 bias[UJ][SUB];
+            auto column = [&](int uj, int k) { return (int)n0 + b_row + 32 * uj + (V == 8 ? dn_joined(lg) : 16 * k + 4 * lg); };
+            auto fetch = [&](int i) {
+#pragma unroll
+                for (int uj = 0; uj < UJ; ++uj) {
+                    if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
+#pragma unroll
+                    for (int k = 0; k < SUB; ++k) {
+                        const int64_t m = m0 + a_row + 16 * i + li;
+                        const int n = column(uj, k);
+                        if (m < P.M && n < P.N) dn_in<EPI, V>(P, m, n, in[i % PRE][uj][k]);
+                    }
+                }
+            };
+            if constexpr (EPI == DN_EPI_LINEAR) {
+                if (P.e.bias) {
+#pragma unroll
+                    for (int uj = 0; uj < UJ; ++uj)
+#pragma unroll
+                        for (int k = 0; k < SUB; ++k) {
+                            DnIn q;
+                            if (column(uj, k) < P.N) dn_raw<V>(P.e.bias, column(uj, k), false, q);
+                            bias[uj][k] = q.a;
+                        }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PRE; ++i) fetch(i);
+#pragma unroll
+            for (int i = 0; i < MS; ++i) {
+                const int64_t m = m0 + a_row + 16 * i + li;
+#pragma unroll
+                for (int uj = 0; uj < UJ; ++uj) {
+                    if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
+                    const float4v v0 = acc[i][2 * uj], v1 = acc[i][2 * uj + 1];
+                    float joined[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    if constexpr (V == 8) dn_join(v0, v1, joined);
+#pragma unroll
+                    for (int k = 0; k < SUB; ++k) {
+                        float v[V];
+#pragma unroll
+                        for (int c = 0; c < V; ++c) v[c] = joined[V * k + c];
+                        const int n = column(uj, k);
+                        if (m < P.M && n < P.N) dn_epi<EPI, V, ACT>(P, m, n, v, in[i % PRE][uj][k], bias[uj][k]);
+                    }
+                }
+                if (i + PRE < MS) fetch(i + PRE);
+            }
+        };
+        if ((EPI == DN_EPI_LINEAR || EPI == DN_EPI_GRAD) && P.e.y_f32)
+            finish(DnInt<4>());
+        else
+            finish(DnInt<8>());
     }
 }
 #endif
 
-template <int BM, int BN, int WM, int WN, int KG, int FORM, int EPI, int ACT>
+template <int BM, int BN, int WM, int WN, int KG, int D, int FORM, int EPI, int ACT>
 __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(DenseParams P) {
 #ifdef __HIP_DEVICE_COMPILE__
-    __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG>];
-    dense_body<BM, BN, WM, WN, KG, FORM, EPI, ACT>(P, blockIdx.x, blockIdx.y, smem);
+    __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG, D>];
+    dense_body<BM, BN, WM, WN, KG, D, FORM, EPI, ACT>(P, blockIdx.x, blockIdx.y, smem);
 #endif
 }
 
@@ -756,26 +847,27 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
 // launch: the input gradient (A B) and up to two weight gradients (A^T B), the
 // one with the longest tiles first.  Apart they would each end in a round of
 // tiles that leaves CUs idle, and wait for the launch before them.
-template <int BM, int BN, int WM, int WN, int KG>
+template <int BM, int BN, int WM, int WN, int KG, int D>
 __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense_grads(DenseGradsParams A) {
 #ifdef __HIP_DEVICE_COMPILE__
-    __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG>];
+    __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG, D>];
     int b = blockIdx.x, i = 0;
     while (b >= A.tiles[i]) b -= A.tiles[i++];  // (the grid is the sum of the tiles)
     if (A.which[i] == 0)
-        dense_body<BM, BN, WM, WN, KG, DN_NN, DN_EPI_LINEAR, DN_ACT_NONE>(A.dx, b, 0, smem);
+        dense_body<BM, BN, WM, WN, KG, D, DN_NN, DN_EPI_LINEAR, DN_ACT_NONE>(A.dx, b, 0, smem);
     else
-        dense_body<BM, BN, WM, WN, KG, DN_TN, DN_EPI_GRAD, DN_ACT_NONE>(A.dw[A.which[i] - 1], b, 0, smem);
+        dense_body<BM, BN, WM, WN, KG, D, DN_TN, DN_EPI_GRAD, DN_ACT_NONE>(A.dw[A.which[i] - 1], b, 0, smem);
 #endif
 }
 
 // launch(tile shape...) for a tile
 #define DN_TILE_SWITCH(tile, LAUNCH)                             \
     switch (tile) {                                              \
-        case DN_TILE_256x256: LAUNCH(512, 256, 256, 2, 4, 1); break; \
-        case DN_TILE_256x128: LAUNCH(512, 256, 128, 4, 2, 1); break; \
-        case DN_TILE_128x128: LAUNCH(512, 128, 128, 2, 2, 2); break; \
-        case DN_TILE_64x64: LAUNCH(1024, 64, 64, 2, 2, 4); break;    \
+        case DN_TILE_256x256: LAUNCH(512, 256, 256, 2, 4, 1, 2); break; \
+        case DN_TILE_256x128: LAUNCH(512, 256, 128, 4, 2, 1, 2); break; \
+        case DN_TILE_128x128: LAUNCH(512, 128, 128, 2, 2, 2, 2); break; \
+        case DN_TILE_128x64: LAUNCH(512, 128, 64, 2, 2, 2, 3); break;   \
+        case DN_TILE_64x64: LAUNCH(1024, 64, 64, 2, 2, 4, 2); break;    \
         default: return hipErrorInvalidValue;                    \
     }
 

@@ -70,8 +70,8 @@ struct TileCost {
     double fixed, step;  // us
 };
 constexpr TileCost TILES[DN_TILES] = {
-    {256, 256, 1, 5.2, 1.22}, {256, 128, 1, 2.9, 0.71}, {128, 128, 2, 3.0, 0.77}, {64, 64, 4, 2.35, 0.74}};
-constexpr double US_LAUNCH = 1.6, US_JOIN = 2.0, US_PER_MB = 0.3, US_PER_PART_MB = 0.82;
+    {256, 256, 1, 5.1, 1.19}, {256, 128, 1, 3.1, 0.70}, {128, 128, 2, 3.5, 0.76}, {128, 64, 2, 2.6, 0.54}, {64, 64, 4, 2.6, 0.70}};
+constexpr double US_LAUNCH = 1.35, US_JOIN = 2.5, US_PER_MB = 0.285, US_PER_PART_MB = 0.74;
 constexpr int CUS = 256;  // (workspace sizes do not depend on the device at hand)
 
 double tile_us(const TileCost &c, int64_t steps) { return c.fixed + c.step * (double)ceil_div(steps, c.groups); }

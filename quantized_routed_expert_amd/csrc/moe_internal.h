@@ -338,7 +338,7 @@ struct DenseRowsParams {
 // along n), C = A^T B (rows of A run along m, of B along n)
 enum DenseForm { DN_NT = 0, DN_NN = 1, DN_TN = 2 };
 enum DenseEpiKind { DN_EPI_LINEAR = 0, DN_EPI_GATED = 1, DN_EPI_DGATED = 2, DN_EPI_GRAD = 3 };
-enum DenseTile { DN_TILE_256x256 = 0, DN_TILE_256x128 = 1, DN_TILE_128x128 = 2, DN_TILE_64x64 = 3, DN_TILES = 4 };
+enum DenseTile { DN_TILE_256x256 = 0, DN_TILE_256x128, DN_TILE_128x128, DN_TILE_128x64, DN_TILE_64x64, DN_TILES };
 
 // dz = dy * act'(z) and the column sums of dz over row chunks
 struct DzParams {
