@@ -170,14 +170,6 @@ __device__ __forceinline__ float dn_act1(int act, float v, float &d) {
             return v;
     }
 }
-// ACT of the epilogues: an activation, or DN_ACT_ANY: e.act, looked at at run
-// time (with the switch in each of a tile's unrolled units the code outgrows
-// the instruction cache: 256 x 256 tiles took 5 us longer)
-constexpr int DN_ACT_ANY = -1;
-template <int ACT>
-__device__ __forceinline__ int dn_act_of(const DenseEpi &e) {
-    return ACT == DN_ACT_ANY ? e.act : ACT;
-}
 template <int V>
 __device__ __forceinline__ void dn_act(int act, float (&v)[V]) {
     float d;
@@ -220,27 +212,11 @@ __device__ __forceinline__ bool dn_last(uint32_t *counter, uint32_t n, uint32_t 
 }
 
 // ---------------------------------------------------------------------------
-// Epilogues: V consecutive columns from n on of row m.  What an epilogue reads
-// at its place (DnIn: a residual, kept gate and up, a gradient to add to) is
-// loaded apart, so that a tile's loads can go out ahead of their use.
+// Results: V consecutive columns.  The few-row kernel's go through pointers,
+// a tile's through buffers whose range is the tile's rows: what lies past the
+// last row or column is neither read nor written, without a branch, so a
+// tile's loads stay in flight (with branches every wait was for all of them).
 // ---------------------------------------------------------------------------
-struct DnIn {
-    u32x4 a, b;
-};
-// raw values: V = 4 takes 8 (bf16) or 16 bytes, V = 8 16 or 32
-template <int V>
-__device__ __forceinline__ void dn_raw(const void *p, int64_t at, bool f32, DnIn &in) {
-    if (f32) {
-        in.a = *(const u32x4 *)((const float *)p + at);
-        if constexpr (V == 8) in.b = *(const u32x4 *)((const float *)p + at + 4);
-    } else if constexpr (V == 8) {
-        in.a = *(const u32x4 *)((const uint16_t *)p + at);
-    } else {
-        const u32x2 q = *(const u32x2 *)((const uint16_t *)p + at);
-        in.a.x = q.x;
-        in.a.y = q.y;
-    }
-}
 // two bf16 in each of V / 2 words
 template <int V>
 __device__ __forceinline__ void dn_unpack(u32x4 q, float (&v)[V]) {
@@ -252,53 +228,51 @@ __device__ __forceinline__ void dn_unpack(u32x4 q, float (&v)[V]) {
     }
 }
 template <int V>
-__device__ __forceinline__ void dn_add_raw(const DnIn &in, bool f32, float (&v)[V]) {
-    if (f32) {
-        const uint32_t w[8] = {in.a.x, in.a.y, in.a.z, in.a.w, in.b.x, in.b.y, in.b.z, in.b.w};
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += __builtin_bit_cast(float, w[i]);
-    } else {
-        float r[V];
-        dn_unpack<V>(in.a, r);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += r[i];
-    }
-}
-template <int V>
-__device__ __forceinline__ void dn_store(void *p, int64_t at, bool f32, const float (&v)[V]) {
-    if (f32)
-        dn_store_f32<V>((float *)p + at, v);
+__device__ __forceinline__ u32x4 dn_packed(const float (&v)[V]) {
+    if constexpr (V == 8)
+        return u32x4{dn_pack(v[0], v[1]), dn_pack(v[2], v[3]), dn_pack(v[4], v[5]), dn_pack(v[6], v[7])};
     else
-        dn_store_bf<V>((uint16_t *)p + at, v);
+        return u32x4{dn_pack(v[0], v[1]), dn_pack(v[2], v[3]), 0u, 0u};
 }
 
 // z = v + bias (kept in bf16 if asked); y = act(z) + residual
-template <int V, int ACT>
-__device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V], const DnIn &in,
-                                              u32x4 bias) {
+template <int V>
+__device__ __forceinline__ void dn_epi_linear(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V]) {
     const int64_t at = m * N + n;
     if (e.bias) {
         float b[V];
-        dn_unpack<V>(bias, b);
+        dn_load_bf<V>(e.bias + n, b);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] += b[i];
     }
     if (e.z) dn_store_bf<V>(e.z + at, v);
-    if (dn_act_of<ACT>(e) != DN_ACT_NONE) dn_act<V>(dn_act_of<ACT>(e), v);
-    if (e.res) dn_add_raw<V>(in, e.res_f32, v);
-    dn_store<V>(e.y, at, e.y_f32, v);
+    if (e.act != DN_ACT_NONE) dn_act<V>(e.act, v);
+    if (e.res) {
+        float r[V];
+        if (e.res_f32)
+            dn_load_f32<V>((const float *)e.res + at, r);
+        else
+            dn_load_bf<V>((const uint16_t *)e.res + at, r);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += r[i];
+    }
+    if (e.y_f32)
+        dn_store_f32<V>((float *)e.y + at, v);
+    else
+        dn_store_bf<V>((uint16_t *)e.y + at, v);
 }
-// h = act(g) u.  h enters the down product in bf16; with h_terms = 3 (an fp32
-// y) as three exact bf16 terms, so that y is as good as its type.  g and u
-// kept for the backward pass are rounded to bf16 (the type that pass reads).
-template <int V, int ACT>
+// h = act(g) u.  h enters the down product in bf16; for an fp32 y exactly, as
+// fp32 (h_terms = 0: split where it is read) or three bf16 terms, so that y is
+// as good as its type.  g and u kept for the backward pass are rounded to
+// bf16 (the type that pass reads).
+template <int V>
 __device__ __forceinline__ void dn_epi_gated(const DenseEpi &e, int64_t M, int N, int64_t m, int n, float (&g)[V],
                                              float (&u)[V]) {
     if (e.gu) {
         dn_store_bf<V>(e.gu + m * (2 * (int64_t)N) + n, g);
         dn_store_bf<V>(e.gu + m * (2 * (int64_t)N) + N + n, u);
     }
-    dn_act<V>(dn_act_of<ACT>(e), g);
+    dn_act<V>(e.act, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] *= u[i];
     if (e.h_terms == 0)
@@ -308,60 +282,45 @@ __device__ __forceinline__ void dn_epi_gated(const DenseEpi &e, int64_t M, int N
     else
         dn_store_bf<V>(e.h + m * N + n, g);
 }
-// v = dh: h = act(g) u, dg = dh u act'(g), du = dh act(g), each rounded once
-// to bf16, the type their products take
-template <int V, int ACT>
-__device__ __forceinline__ void dn_epi_dgated(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V], const DnIn &in) {
-    float g[V], u[V], h[V], dg[V], du[V];
-    const int64_t at = m * (2 * (int64_t)N) + n;
-    dn_unpack<V>(in.a, g);
-    dn_unpack<V>(in.b, u);
+
+#ifdef __HIP_DEVICE_COMPILE__
+// A tile's rows of a matrix of `ld` columns: element offsets from its first
+// row; a null matrix is empty.
+constexpr int DN_NO_COLUMN = 1 << 29;  // past the range of every tile, in elements of 2 and of 4 bytes
+struct DnRows {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ DnRows(const void *p, int64_t m0, int rows, int64_t ld, int size) {
+        r = __builtin_amdgcn_make_buffer_rsrc((uint8_t *)const_cast<void *>(p) + (p ? m0 * ld * size : 0), (short)0,
+                                              p ? rows * (int)ld * size : 0, 0x00027000);
+    }
+    __device__ __forceinline__ u32x4 load16(int off) const { return __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0); }
+    __device__ __forceinline__ u32x4 load8(int off) const {
+        const u32x2 q = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+        return u32x4{q.x, q.y, 0u, 0u};
+    }
+    __device__ __forceinline__ void store16(u32x4 v, int off) const { __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0); }
+    __device__ __forceinline__ void store8(u32x4 v, int off) const {
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, r, off, 0, 0);
+    }
+    // V bf16 from element `at` on
+    template <int V>
+    __device__ __forceinline__ u32x4 load_bf(int at) const {
+        return V == 8 ? load16(2 * at) : load8(2 * at);
+    }
+    template <int V>
+    __device__ __forceinline__ void store_bf(const float (&v)[V], int at) const {
+        if (V == 8)
+            store16(dn_packed<V>(v), 2 * at);
+        else
+            store8(dn_packed<V>(v), 2 * at);
+    }
+    template <int V>
+    __device__ __forceinline__ void store_words(const uint32_t (&w)[V], int at) const {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        float d;
-        const float a = dn_act1<true>(dn_act_of<ACT>(e), g[i], d);
-        h[i] = a * u[i];
-        dg[i] = v[i] * u[i] * d;
-        du[i] = v[i] * a;
+        for (int i = 0; i < V; i += 4) store16(u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]}, 4 * (at + i));
     }
-    if (e.h) dn_store_bf<V>(e.h + m * N + n, h);
-    dn_store_bf<V>(e.dgu + at, dg);
-    dn_store_bf<V>(e.dgu + at + N, du);
-}
-// weight gradient: row m of y, or of y2 from m_split on (either may be null);
-// accumulate: on what is there, in its own type
-template <int V>
-__device__ __forceinline__ void dn_epi_grad(const DenseEpi &e, int N, int64_t m, int n, float (&v)[V], const DnIn &in) {
-    const bool second = m >= e.m_split;
-    void *const y = second ? e.y2 : e.y;
-    if (!y) return;
-    if (e.accumulate) dn_add_raw<V>(in, e.y_f32, v);
-    dn_store<V>(y, (second ? m - e.m_split : m) * N + n, e.y_f32, v);
-}
-// an epilogue's input, if it has one
-template <int EPI, int V>
-__device__ __forceinline__ void dn_in(const DenseParams &P, int64_t m, int n, DnIn &in) {
-    const DenseEpi &e = P.e;
-    if constexpr (EPI == DN_EPI_LINEAR) {
-        if (e.res) dn_raw<V>(e.res, m * P.N + n, e.res_f32, in);
-    }
-    if constexpr (EPI == DN_EPI_DGATED) {
-        const uint16_t *p = e.gu_in + m * (2 * (int64_t)P.N) + n;
-        in.a = *(const u32x4 *)p;
-        in.b = *(const u32x4 *)(p + P.N);
-    }
-    if constexpr (EPI == DN_EPI_GRAD) {
-        const bool second = m >= e.m_split;
-        const void *const y = second ? e.y2 : e.y;
-        if (e.accumulate && y) dn_raw<V>(y, (second ? m - e.m_split : m) * P.N + n, e.y_f32, in);
-    }
-}
-template <int EPI, int V, int ACT>
-__device__ __forceinline__ void dn_epi(const DenseParams &P, int64_t m, int n, float (&v)[V], const DnIn &in, u32x4 bias) {
-    if constexpr (EPI == DN_EPI_LINEAR) dn_epi_linear<V, ACT>(P.e, P.N, m, n, v, in, bias);
-    if constexpr (EPI == DN_EPI_DGATED) dn_epi_dgated<V, ACT>(P.e, P.N, m, n, v, in);
-    if constexpr (EPI == DN_EPI_GRAD) dn_epi_grad<V>(P.e, P.N, m, n, v, in);
-}
+};
+#endif
 
 // ---------------------------------------------------------------------------
 // Streaming one operand's slices into LDS
@@ -745,70 +704,119 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
                 for (int j = 0; j < UB; ++j) acc[i][uj * UB + j] = v[j];
             }
     }
+    auto row = [&](int i) { return a_row + 16 * i + li; };  // of the tile
+    const int N = P.N;
     if constexpr (GATED) {
+        constexpr int V = JP == 2 ? 8 : 4;
+        const DenseEpi &e = P.e;
+        const int64_t plane = (int64_t)P.M * N;
+        const DnRows gu(e.gu, m0, rows, 2 * (int64_t)N, 2);
+        const DnRows h0(e.h, m0, rows, N, 2), h1(e.h_terms == 3 ? e.h + plane : nullptr, m0, rows, N, 2),
+            h2(e.h_terms == 3 ? e.h + 2 * plane : nullptr, m0, rows, N, 2), hf(e.h_terms == 0 ? e.h : nullptr, m0, rows, N, 4);
 #pragma unroll
         for (int i = 0; i < MS; ++i) {
-            const int64_t m = m0 + a_row + 16 * i + li;
 #pragma unroll
             for (int uj = 0; uj < UJ; ++uj) {
                 if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
                 const int j0 = uj * 2 * JP;
-                const int nb = (int)n0 + (b_row >> 1) + 16 * JP * uj;  // first column of the unit
+                float g[V], u[V];
                 if constexpr (JP == 2) {
-                    float gv[8], uv[8];
-                    dn_join(acc[i][j0], acc[i][j0 + 2], gv);
-                    dn_join(acc[i][j0 + 1], acc[i][j0 + 3], uv);
-                    const int n = nb + dn_joined(lg);
-                    if (m < P.M && n < P.N) dn_epi_gated<8, ACT>(P.e, P.M, P.N, m, n, gv, uv);
+                    dn_join(acc[i][j0], acc[i][j0 + 2], g);
+                    dn_join(acc[i][j0 + 1], acc[i][j0 + 3], u);
                 } else {
-                    const float4v g = acc[i][j0], u = acc[i][j0 + 1];
-                    float gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
-                    const int n = nb + 4 * lg;
-                    if (m < P.M && n < P.N) dn_epi_gated<4, ACT>(P.e, P.M, P.N, m, n, gv, uv);
+                    const float4v a = acc[i][j0], b = acc[i][j0 + 1];
+                    g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+                    u[0] = b.x, u[1] = b.y, u[2] = b.z, u[3] = b.w;
+                }
+                int n = (int)n0 + (b_row >> 1) + 16 * JP * uj + (JP == 2 ? dn_joined(lg) : 4 * lg);
+                n = n < N ? n : DN_NO_COLUMN;
+                if (e.gu) {
+                    gu.template store_bf<V>(g, 2 * row(i) * N + n);
+                    gu.template store_bf<V>(u, 2 * row(i) * N + N + n);
+                }
+                dn_act<V>(ACT, g);
+#pragma unroll
+                for (int k = 0; k < V; ++k) g[k] *= u[k];
+                const int at = row(i) * N + n;
+                // (h's roundings: see dn_epi_gated)
+                if (e.h_terms == 1) {
+                    h0.template store_bf<V>(g, at);
+                } else if (e.h_terms == 3) {
+                    uint32_t t[V][3];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) dn_split3(g[k], t[k]);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        u32x4 w = {dn_high2(t[0][q], t[1][q]), dn_high2(t[2][q], t[3][q]), 0u, 0u};
+                        if constexpr (V == 8) {
+                            w.z = dn_high2(t[4][q], t[5][q]);
+                            w.w = dn_high2(t[6][q], t[7][q]);
+                        }
+                        const DnRows &h = q == 0 ? h0 : q == 1 ? h1 : h2;
+                        if (V == 8)
+                            h.store16(w, 2 * at);
+                        else
+                            h.store8(w, 2 * at);
+                    }
+                } else {
+                    uint32_t w[V];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) w[k] = __builtin_bit_cast(uint32_t, g[k]);
+                    hf.template store_words<V>(w, at);
                 }
             }
         }
     } else {
         // V = 8: a unit's joined blocks (bf16 results); V = 4: fp32 results,
-        // where four columns are 16 bytes and a row's four lanes 64
-        auto finish = [&](auto width) {
-            constexpr int V = decltype(width)::value, SUB = 8 / V;
-            // what row blocks i .. i + PRE - 1 read is in flight while block i
-            // is finished (one at a time, 256 x 256 tiles with an fp32
-            // residual took 30 us longer)
-            constexpr int PRE = MS < 4 ? MS : 4;
-            DnIn in[PRE][UJ][SUB];
-            u32x4 bias[UJ][SUB];
-            auto column = [&](int uj, int k) { return (int)n0 + b_row + 32 * uj + (V == 8 ? dn_joined(lg) : 16 * k + 4 * lg); };
+        // where four columns are 16 bytes and a row's four lanes 64.  IN: what
+        // is read at a result's place: 0 nothing, 1 bf16 values (a residual),
+        // 2 fp32 values, 3 gate and up.
+        auto finish = [&](auto width, auto reads) {
+            constexpr int V = decltype(width)::value, IN = decltype(reads)::value, SUB = 8 / V;
+            const DenseEpi &e = P.e;
+            // row blocks whose input is in flight ahead of their use
+            constexpr int AHEAD = IN == 0 ? 1 : IN == 2 && V == 8 ? 2 : 4;  // (what the registers hold)
+            constexpr int PRE = MS < AHEAD ? MS : AHEAD;
+            constexpr int LD = EPI == DN_EPI_DGATED ? 2 : 1;
+            u32x4 in[PRE][UJ][SUB][2];
+            int col[UJ][SUB];
+            float bias[UJ][SUB][V];
+            const DnRows from(EPI == DN_EPI_DGATED ? e.gu_in : e.res, m0, rows, LD * (int64_t)N, IN == 2 ? 4 : 2);
+            const DnRows brow(EPI == DN_EPI_LINEAR ? e.bias : nullptr, 0, 1, N, 2);
+#pragma unroll
+            for (int uj = 0; uj < UJ; ++uj)
+#pragma unroll
+                for (int k = 0; k < SUB; ++k) {
+                    const int n = (int)n0 + b_row + 32 * uj + (V == 8 ? dn_joined(lg) : 16 * k + 4 * lg);
+                    col[uj][k] = n < N ? n : DN_NO_COLUMN;
+                    if constexpr (EPI == DN_EPI_LINEAR) dn_unpack<V>(brow.template load_bf<V>(col[uj][k]), bias[uj][k]);
+                }
             auto fetch = [&](int i) {
+                if constexpr (IN > 0) {
 #pragma unroll
-                for (int uj = 0; uj < UJ; ++uj) {
-                    if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
+                    for (int uj = 0; uj < UJ; ++uj) {
+                        if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
 #pragma unroll
-                    for (int k = 0; k < SUB; ++k) {
-                        const int64_t m = m0 + a_row + 16 * i + li;
-                        const int n = column(uj, k);
-                        if (m < P.M && n < P.N) dn_in<EPI, V>(P, m, n, in[i % PRE][uj][k]);
+                        for (int k = 0; k < SUB; ++k) {
+                            const int at = LD * row(i) * N + col[uj][k];
+                            u32x4(&q)[2] = in[i % PRE][uj][k];
+                            if constexpr (IN == 2) {
+                                q[0] = from.load16(4 * at);
+                                if constexpr (V == 8) q[1] = from.load16(4 * at + 16);
+                            } else {
+                                q[0] = from.template load_bf<V>(at);
+                                if constexpr (IN == 3) q[1] = from.template load_bf<V>(at + N);
+                            }
+                        }
                     }
                 }
             };
-            if constexpr (EPI == DN_EPI_LINEAR) {
-                if (P.e.bias) {
-#pragma unroll
-                    for (int uj = 0; uj < UJ; ++uj)
-#pragma unroll
-                        for (int k = 0; k < SUB; ++k) {
-                            DnIn q;
-                            if (column(uj, k) < P.N) dn_raw<V>(P.e.bias, column(uj, k), false, q);
-                            bias[uj][k] = q.a;
-                        }
-                }
-            }
+            const DnRows y(e.y, m0, rows, N, V == 4 ? 4 : 2), z(e.z, m0, rows, N, 2);
+            const DnRows dgu(EPI == DN_EPI_DGATED ? e.dgu : nullptr, m0, rows, 2 * (int64_t)N, 2), h(e.h, m0, rows, N, 2);
 #pragma unroll
             for (int i = 0; i < PRE; ++i) fetch(i);
 #pragma unroll
             for (int i = 0; i < MS; ++i) {
-                const int64_t m = m0 + a_row + 16 * i + li;
 #pragma unroll
                 for (int uj = 0; uj < UJ; ++uj) {
                     if (KG > 1 && (i * UJ + uj) % KG != grp) continue;
@@ -820,17 +828,76 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
                         float v[V];
 #pragma unroll
                         for (int c = 0; c < V; ++c) v[c] = joined[V * k + c];
-                        const int n = column(uj, k);
-                        if (m < P.M && n < P.N) dn_epi<EPI, V, ACT>(P, m, n, v, in[i % PRE][uj][k], bias[uj][k]);
+                        const u32x4(&q)[2] = in[i % PRE][uj][k];
+                        if constexpr (EPI == DN_EPI_DGATED) {
+                            // v = dh: h = act(g) u, dg = dh u act'(g), du = dh act(g),
+                            // each rounded once to bf16, the type their products take
+                            float g[V], u[V], hv[V], du[V];
+                            dn_unpack<V>(q[0], g);
+                            dn_unpack<V>(q[1], u);
+#pragma unroll
+                            for (int c = 0; c < V; ++c) {
+                                float d;
+                                const float a = dn_act1<true>(ACT, g[c], d);
+                                hv[c] = a * u[c];
+                                du[c] = v[c] * a;
+                                v[c] = v[c] * u[c] * d;
+                            }
+                            h.template store_bf<V>(hv, row(i) * N + col[uj][k]);
+                            dgu.template store_bf<V>(v, 2 * row(i) * N + col[uj][k]);
+                            dgu.template store_bf<V>(du, 2 * row(i) * N + N + col[uj][k]);
+                        } else {
+                            // z = v + bias, y = act(z) + residual
+                            const int at = row(i) * N + col[uj][k];
+#pragma unroll
+                            for (int c = 0; c < V; ++c) v[c] += bias[uj][k][c];
+                            if (e.z) z.template store_bf<V>(v, at);
+                            if (ACT != DN_ACT_NONE) dn_act<V>(ACT, v);
+                            if constexpr (IN == 1) {
+                                float r[V];
+                                dn_unpack<V>(q[0], r);
+#pragma unroll
+                                for (int c = 0; c < V; ++c) v[c] += r[c];
+                            }
+                            if constexpr (IN == 2) {
+                                const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+                                for (int c = 0; c < V; ++c) v[c] += __builtin_bit_cast(float, w[c]);
+                            }
+                            if constexpr (V == 4) {
+                                uint32_t w[V];
+#pragma unroll
+                                for (int c = 0; c < V; ++c) w[c] = __builtin_bit_cast(uint32_t, v[c]);
+                                y.template store_words<V>(w, at);
+                            } else {
+                                y.template store_bf<V>(v, at);
+                            }
+                        }
                     }
                 }
                 if (i + PRE < MS) fetch(i + PRE);
             }
         };
-        if ((EPI == DN_EPI_LINEAR || EPI == DN_EPI_GRAD) && P.e.y_f32)
-            finish(DnInt<4>());
-        else
-            finish(DnInt<8>());
+        if constexpr (EPI == DN_EPI_DGATED) {
+            finish(DnInt<8>(), DnInt<3>());
+        } else {
+            const int in = !P.e.res ? 0 : P.e.res_f32 ? 2 : 1;
+            if (P.e.y_f32) {
+                if (in == 0)
+                    finish(DnInt<4>(), DnInt<0>());
+                else if (in == 1)
+                    finish(DnInt<4>(), DnInt<1>());
+                else
+                    finish(DnInt<4>(), DnInt<2>());
+            } else {
+                if (in == 0)
+                    finish(DnInt<8>(), DnInt<0>());
+                else if (in == 1)
+                    finish(DnInt<8>(), DnInt<1>());
+                else
+                    finish(DnInt<8>(), DnInt<2>());
+            }
+        }
     }
 }
 #endif
@@ -844,8 +911,8 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
 }
 
 // A backward pass's last products, which do not depend on each other, in one
-// launch: the input gradient (A B) and up to two weight gradients (A^T B), the
-// one with the longest tiles first.  Apart they would each end in a round of
+// launch: the input gradient (A B) and the weight gradients (A^T B), those
+// with the longest tiles first.  Apart they would each end in a round of
 // tiles that leaves CUs idle, and wait for the launch before them.
 template <int BM, int BN, int WM, int WN, int KG, int D>
 __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense_grads(DenseGradsParams A) {
@@ -853,10 +920,10 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense_grads
     __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG, D>];
     int b = blockIdx.x, i = 0;
     while (b >= A.tiles[i]) b -= A.tiles[i++];  // (the grid is the sum of the tiles)
-    if (A.which[i] == 0)
-        dense_body<BM, BN, WM, WN, KG, D, DN_NN, DN_EPI_LINEAR, DN_ACT_NONE>(A.dx, b, 0, smem);
+    if (i == A.dx_at)
+        dense_body<BM, BN, WM, WN, KG, D, DN_NN, DN_EPI_LINEAR, DN_ACT_NONE>(A.p[i], b, 0, smem);
     else
-        dense_body<BM, BN, WM, WN, KG, D, DN_TN, DN_EPI_GRAD, DN_ACT_NONE>(A.dw[A.which[i] - 1], b, 0, smem);
+        dense_body<BM, BN, WM, WN, KG, D, DN_TN, DN_EPI_LINEAR, DN_ACT_NONE>(A.p[i], b, 0, smem);
 #endif
 }
 
@@ -882,7 +949,7 @@ hipError_t dense_tile_t(const DenseParams &P, int tile, hipStream_t st) {
 }
 template <int FORM, int EPI>
 hipError_t dense_launch_t(const DenseParams &P, int tile, hipStream_t st) {
-    constexpr bool A = EPI != DN_EPI_GRAD && !(FORM == DN_NN && EPI == DN_EPI_LINEAR);  // with an activation
+    constexpr bool A = FORM == DN_NT || EPI != DN_EPI_LINEAR;  // with an activation
     switch (A ? P.e.act : DN_ACT_NONE) {
         case DN_ACT_SILU: return dense_tile_t<FORM, EPI, A ? DN_ACT_SILU : 0>(P, tile, st);
         case DN_ACT_GELU: return dense_tile_t<FORM, EPI, A ? DN_ACT_GELU : 0>(P, tile, st);

@@ -230,7 +230,7 @@ GatedWs gated_ws(int64_t T, int64_t H, int64_t F, bool x_f32, bool y_f32) {
     w.down = make_plan(T, H, ksteps(F) * (y_f32 ? 3 : 1));
     w.dh = make_plan(T, F, ksteps(H));
     w.dx = make_plan(T, H, 2 * ksteps(F));
-    w.dw = make_plan(2 * F, H, ksteps(T));
+    w.dw = make_plan(F, H, ksteps(T));
     w.dd = make_plan(H, F, ksteps(T));
     Carve c;
     w.x3 = c.take(x_f32 ? T * H * 6 : 0);
@@ -248,44 +248,31 @@ GatedWs gated_ws(int64_t T, int64_t H, int64_t F, bool x_f32, bool y_f32) {
 inline hipStream_t S(int64_t s) { return (hipStream_t)(intptr_t)s; }
 int launch_err(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 
-// A backward pass's last products, planned apart (pdx, pdw[0..n)): one launch
-// of all where its estimate is lower, else one each.
-int launch_grads(const DenseParams *dx, const Plan &pdx, DenseParams *const *dw, const Plan *pdw, int n, hipStream_t st) {
-    const DenseParams *all[3];
-    int which[3], k = 0;
+// A backward pass's last products (p[0] dx where with_dx, the rest weight
+// gradients), each with the plan of a launch of its own: one launch of all
+// where its estimate is lower.
+int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, hipStream_t st) {
+    int order[DN_MAX_GRADS];
     double apart = 0.0;
-    if (dx) {
-        all[k] = dx;
-        which[k++] = 0;
-        apart += pdx.us;
-    }
-    for (int i = 0; i < n; ++i) {
-        all[k] = dw[i];
-        which[k++] = 1 + i;
-        apart += pdw[i].us;
-    }
-    for (int i = 1; i < k; ++i) {  // longest tiles first
-        for (int j = i; j > 0 && all[j]->steps > all[j - 1]->steps; --j) {
-            const DenseParams *p = all[j];
-            const int w = which[j];
-            all[j] = all[j - 1];
-            which[j] = which[j - 1];
-            all[j - 1] = p;
-            which[j - 1] = w;
-        }
+    for (int i = 0; i < n; ++i) {  // longest tiles first
+        int j = i;
+        for (; j > 0 && p[i].steps > p[order[j - 1]].steps; --j) order[j] = order[j - 1];
+        order[j] = i;
+        apart += plans[i].us;
     }
     int best = -1;
     double best_us = 1e30;
     for (int t = 0; t < DN_TILES; ++t) {
         const TileCost &c = TILES[t];
-        double us[3], out = 0.0;
-        int64_t tiles[3];
-        for (int i = 0; i < k; ++i) {
-            us[i] = tile_us(c, all[i]->steps);
-            tiles[i] = ceil_div(all[i]->M, c.bm) * ceil_div(all[i]->N, c.bn);
-            out += out_us(all[i]->M, all[i]->N);
+        double us[DN_MAX_GRADS], out = 0.0;
+        int64_t tiles[DN_MAX_GRADS];
+        for (int i = 0; i < n; ++i) {
+            const DenseParams &q = p[order[i]];
+            us[i] = tile_us(c, q.steps);
+            tiles[i] = ceil_div(q.M, c.bm) * ceil_div(q.N, c.bn);
+            out += out_us(q.M, q.N);
         }
-        const double all_us = US_LAUNCH + out + tiles_us(us, tiles, k);
+        const double all_us = US_LAUNCH + out + tiles_us(us, tiles, n);
         if (all_us < best_us) {
             best_us = all_us;
             best = t;
@@ -295,26 +282,43 @@ int launch_grads(const DenseParams *dx, const Plan &pdx, DenseParams *const *dw,
     if (g_force_merge == 9) best_us = 1e30;
     if (g_force_merge >= 0 && g_force_merge < 9) { best = g_force_merge; best_us = 0; }
 #endif
-    if (k < 2 || apart <= best_us) {
-        if (dx && dense_dx_launch(*dx, pdx.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
-        for (int i = 0; i < n; ++i)
-            if (dense_dw_launch(*dw[i], pdw[i].tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
+    if (n < 2 || apart <= best_us) {
+        for (int i = 0; i < n; ++i) {
+            const hipError_t e = i == 0 && with_dx ? dense_dx_launch(p[i], plans[i].tile, st) : dense_dw_launch(p[i], plans[i].tile, st);
+            if (e != hipSuccess) return MOE_ERR_LAUNCH;
+        }
         return MOE_OK;
     }
     DenseGradsParams A;
     memset(&A, 0, sizeof(A));
+    A.n = n;
+    A.dx_at = -1;
     const TileCost &c = TILES[best];
-    for (int i = 0; i < k; ++i) {
-        DenseParams &P = which[i] == 0 ? A.dx : A.dw[which[i] - 1];
-        P = *all[i];
-        P.tiles_m = (int)ceil_div(P.M, c.bm);
-        P.tiles_n = (int)ceil_div(P.N, c.bn);
-        P.splits = 1;
-        P.steps_per_split = P.steps > 0 ? P.steps : 1;
-        A.which[i] = which[i];
-        A.tiles[i] = P.tiles_m * P.tiles_n;
+    for (int i = 0; i < n; ++i) {
+        DenseParams &q = A.p[i];
+        q = p[order[i]];
+        q.tiles_m = (int)ceil_div(q.M, c.bm);
+        q.tiles_n = (int)ceil_div(q.N, c.bn);
+        q.splits = 1;
+        q.steps_per_split = q.steps > 0 ? q.steps : 1;
+        A.tiles[i] = q.tiles_m * q.tiles_n;
+        if (with_dx && order[i] == 0) A.dx_at = i;
     }
     return launch_err(dense_grads_launch(A, best, st));
+}
+
+// A weight gradient A^T B over T rows, into y or onto it
+DenseParams grad_params(const DenseSeg &g, const Plan &plan, int M, int N, int T, void *y, int32_t dtype, int32_t accumulate,
+                        void *ws, int64_t part) {
+    DenseParams P;
+    memset(&P, 0, sizeof(P));
+    P.nseg = 1;
+    P.seg[0] = g;
+    set_plan(P, plan, M, N, (int)ksteps(T), ws, part);
+    P.e.y = y;
+    P.e.y_f32 = P.e.res_f32 = dtype == MOE_DTYPE_F32;
+    P.e.res = accumulate ? y : nullptr;
+    return P;
 }
 
 // x's products with rows of K: one (bf16) or three (fp32, its exact bf16
@@ -436,26 +440,25 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
         ColsumParams C{(const float *)at(ws, L.chunks), dbias, out, nchunks, dw_dtype == MOE_DTYPE_F32, accumulate != 0};
         if (dense_colsum_launch(C, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
-    DenseParams X, W, *const dws[1] = {&W};
-    memset(&X, 0, sizeof(X));
-    memset(&W, 0, sizeof(W));
+    DenseParams P[2];
+    Plan plans[2];
+    int n = 0;
     const bool with_dx = dx && T != 0;
     if (with_dx) {
+        DenseParams &X = P[n];
+        memset(&X, 0, sizeof(X));
         X.nseg = 1;
         X.seg[0] = DenseSeg{dz, (const uint16_t *)w, nullptr, out, in, out};
         set_plan(X, L.dx, T, in, (int)ksteps(out), ws, L.bpart);
         X.e.y = dx;
+        plans[n++] = L.dx;
     }
     if (dw) {
-        W.nseg = 1;
-        W.seg[0] = DenseSeg{dz, (const uint16_t *)x, nullptr, out, in, T};
-        set_plan(W, L.dw, out, in, (int)ksteps(T), ws, L.bpart);
-        W.e.y = dw;
-        W.e.m_split = out;
-        W.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
-        W.e.accumulate = accumulate != 0;
+        P[n] = grad_params(DenseSeg{dz, (const uint16_t *)x, nullptr, out, in, T}, L.dw, out, in, T, dw, dw_dtype, accumulate, ws,
+                           L.bpart);
+        plans[n++] = L.dw;
     }
-    return launch_grads(with_dx ? &X : nullptr, L.dx, dws, &L.dw, dw ? 1 : 0, st);
+    return launch_grads(P, plans, n, with_dx, st);
 }
 
 int64_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t hidden, int32_t ffn) {
@@ -566,38 +569,29 @@ int moe_gated_ffn_backward(const void *dy, const void *x, int32_t T, const moe_d
         P.e.h = ddown ? h : nullptr;
         if (dense_dgated_launch(P, L.dh.tile, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
-    DenseParams X, W[2], *dws[2];
-    memset(&X, 0, sizeof(X));
-    memset(W, 0, sizeof(W));
-    Plan pdw[2];
+    DenseParams P[DN_MAX_GRADS];
+    Plan plans[DN_MAX_GRADS];
     int n = 0;
     const bool with_dx = dx && T != 0;
     if (with_dx) {  // dx = dg Wg + du Wu
+        DenseParams &X = P[n];
+        memset(&X, 0, sizeof(X));
         X.nseg = 2;
         X.seg[0] = DenseSeg{dgu, (const uint16_t *)w->gate, nullptr, 2 * (int64_t)F, H, F};
         X.seg[1] = DenseSeg{dgu + F, (const uint16_t *)w->up, nullptr, 2 * (int64_t)F, H, F};
         set_plan(X, L.dx, T, H, (int)(2 * ksteps(F)), ws, L.bpart);
         X.e.y = dx;
+        plans[n++] = L.dx;
     }
-    auto grad = [&](const DenseSeg &g, const Plan &p, int M, int N, void *y, void *y2, int m_split) {
-        DenseParams &P = W[n];
-        P.nseg = 1;
-        P.seg[0] = g;
-        set_plan(P, p, M, N, (int)ksteps(T), ws, L.bpart);
-        P.e.y = y;
-        P.e.y2 = y2;
-        P.e.m_split = m_split;
-        P.e.y_f32 = dw_dtype == MOE_DTYPE_F32;
-        P.e.accumulate = accumulate != 0;
-        pdw[n] = p;
-        dws[n] = &P;
-        ++n;
+    auto grad = [&](const uint16_t *a, int64_t lda, const void *b, int M, int N, const Plan &plan, void *y) {
+        if (!y) return;
+        P[n] = grad_params(DenseSeg{a, (const uint16_t *)b, nullptr, lda, N, T}, plan, M, N, T, y, dw_dtype, accumulate, ws, L.bpart);
+        plans[n++] = plan;
     };
-    if (dgate || dup)  // [dg du]^T x
-        grad(DenseSeg{dgu, (const uint16_t *)x, nullptr, 2 * (int64_t)F, H, T}, L.dw, 2 * F, H, dgate, dup, F);
-    if (ddown)  // dy^T h
-        grad(DenseSeg{(const uint16_t *)dy, h, nullptr, H, F, T}, L.dd, H, F, ddown, nullptr, H);
-    return launch_grads(with_dx ? &X : nullptr, L.dx, dws, pdw, n, st);
+    grad(dgu, 2 * (int64_t)F, x, F, H, L.dw, dgate);
+    grad(dgu + F, 2 * (int64_t)F, x, F, H, L.dw, dup);
+    grad((const uint16_t *)dy, H, h, H, F, L.dd, ddown);
+    return launch_grads(P, plans, n, with_dx, st);
 }
 
 }  // extern "C"

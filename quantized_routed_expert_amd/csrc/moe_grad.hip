@@ -9,10 +9,12 @@ hipError_t dense_dx_launch(const DenseParams &P, int tile, hipStream_t st) {
     return dense_launch_t<DN_NN, DN_EPI_LINEAR>(P, tile, st);
 }
 hipError_t dense_dw_launch(const DenseParams &P, int tile, hipStream_t st) {
-    return dense_launch_t<DN_TN, DN_EPI_GRAD>(P, tile, st);
+    return dense_launch_t<DN_TN, DN_EPI_LINEAR>(P, tile, st);
 }
 hipError_t dense_grads_launch(const DenseGradsParams &A, int tile, hipStream_t st) {
-    const dim3 grid((unsigned)(A.tiles[0] + A.tiles[1] + A.tiles[2]));
+    int64_t tiles = 0;
+    for (int i = 0; i < A.n; ++i) tiles += A.tiles[i];
+    const dim3 grid((unsigned)tiles);
 #define DN_LAUNCH(THREADS, ...) hipLaunchKernelGGL((k_dense_grads<__VA_ARGS__>), grid, dim3(THREADS), 0, st, A)
     DN_TILE_SWITCH(tile, DN_LAUNCH)
 #undef DN_LAUNCH

@@ -295,14 +295,12 @@ struct DenseEpi {
     const uint16_t *bias;  // [N] or null
     const void *res;       // [M][N] or null
     void *y;               // [M][N]
-    void *y2;              // weight gradients: the rows from m_split on
     uint16_t *z;           // [M][N] pre-activation or null
     uint16_t *h;           // gated: h_terms planes of [M][N]
     uint16_t *gu;          // gated: [M][2N] gate and up, kept (or null)
     const uint16_t *gu_in;  // gated backward: the kept gate and up
     uint16_t *dgu;          // gated backward: their gradients [M][2N]
-    int m_split;
-    int act, y_f32, res_f32, accumulate;
+    int act, y_f32, res_f32;
     int h_terms;  // 1 or 3 bf16 terms; 0: h is one plane of fp32
 };
 
@@ -317,11 +315,13 @@ struct DenseParams {
     int splits, steps_per_split;
 };
 
-// The products of a backward pass that run side by side: which[i] is 0 (dx)
-// or 1 + the index of a weight gradient, tiles[i] its tiles.
+// The products of a backward pass that run side by side, longest tiles first:
+// p[dx_at] is dx (A B; -1: none), the others weight gradients (A^T B);
+// tiles[i]: the tiles of p[i].
+constexpr int DN_MAX_GRADS = 4;
 struct DenseGradsParams {
-    DenseParams dx, dw[2];
-    int which[3], tiles[3];
+    DenseParams p[DN_MAX_GRADS];
+    int tiles[DN_MAX_GRADS], n, dx_at;
 };
 
 // Few rows (a decode window): C = A B^T by streaming B once, k split over
@@ -337,7 +337,7 @@ struct DenseRowsParams {
 // product forms: C = A B^T (rows of both run along k), C = A B (B's rows run
 // along n), C = A^T B (rows of A run along m, of B along n)
 enum DenseForm { DN_NT = 0, DN_NN = 1, DN_TN = 2 };
-enum DenseEpiKind { DN_EPI_LINEAR = 0, DN_EPI_GATED = 1, DN_EPI_DGATED = 2, DN_EPI_GRAD = 3 };
+enum DenseEpiKind { DN_EPI_LINEAR = 0, DN_EPI_GATED = 1, DN_EPI_DGATED = 2 };
 enum DenseTile { DN_TILE_256x256 = 0, DN_TILE_256x128, DN_TILE_128x128, DN_TILE_128x64, DN_TILE_64x64, DN_TILES };
 
 // dz = dy * act'(z) and the column sums of dz over row chunks

@@ -138,12 +138,9 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
     sum(v, c);
     if constexpr (GATED) {
         sum(u, RN + c);
-        dn_epi_gated<4, DN_ACT_ANY>(P.e, P.M, P.N, m, n0 + c, v, u);
+        dn_epi_gated<4>(P.e, P.M, P.N, m, n0 + c, v, u);
     } else {
-        DnIn in, bias;
-        if (P.e.res) dn_raw<4>(P.e.res, (int64_t)m * P.N + n0 + c, P.e.res_f32, in);
-        if (P.e.bias) dn_raw<4>(P.e.bias, n0 + c, false, bias);
-        dn_epi_linear<4, DN_ACT_ANY>(P.e, P.N, m, n0 + c, v, in, bias.a);
+        dn_epi_linear<4>(P.e, P.N, m, n0 + c, v);
     }
 }
 
