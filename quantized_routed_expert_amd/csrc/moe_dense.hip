@@ -60,18 +60,19 @@ struct Plan {
 // The least estimated time over the tiles and split counts.  Rounds of one
 // tile per CU; a tile takes a fixed time and one per step (of its longest
 // group), the results one per MB, a split the hand-over and the parts'
-// traffic.  Fitted to the launches of 57 products (16 x 2048 x 768 to
-// 8192 x 4096 x 11008, each tile, splits of 1 to 16) that are within 1.9 times
-// the best of their product: 11% off in the mean, and the choice costs 1% over
-// the best.  E.g. 2048 x 2048 outputs over 512 k take 10 us in 128 x 128 tiles
-// and 20 in 64 x 64; 2048 x 512 outputs over 2048 k 17 and 10.
+// traffic.  Fitted to the launches of 63 products (16 x 2048 x 768 to
+// 8192 x 4096 x 11008, each tile, splits of 1, 2 and 4) that are within 1.9
+// times the best of their product: 8% off in the mean, and the choice costs
+// 0.1% over the best.  E.g. 2048 x 2048 outputs over 512 k take 10 us in
+// 128 x 128 tiles and 20 in 64 x 64; 2048 x 512 outputs over 2048 k 17 and 10;
+// 2048 x 1024 outputs over 2048 k 18, 19 and in 128 x 64 tiles 14.6.
 struct TileCost {
     int bm, bn, groups;
     double fixed, step;  // us
 };
 constexpr TileCost TILES[DN_TILES] = {
-    {256, 256, 1, 5.1, 1.19}, {256, 128, 1, 3.1, 0.70}, {128, 128, 2, 3.5, 0.76}, {128, 64, 2, 2.6, 0.54}, {64, 64, 4, 2.6, 0.70}};
-constexpr double US_LAUNCH = 1.35, US_JOIN = 2.5, US_PER_MB = 0.285, US_PER_PART_MB = 0.74;
+    {256, 256, 1, 4.6, 1.21}, {256, 128, 1, 2.9, 0.72}, {128, 128, 2, 3.9, 0.76}, {128, 64, 2, 3.0, 0.53}, {64, 64, 4, 2.7, 0.70}};
+constexpr double US_LAUNCH = 1.4, US_JOIN = 2.6, US_PER_MB = 0.18, US_PER_PART_MB = 0.6;
 constexpr int CUS = 256;  // (workspace sizes do not depend on the device at hand)
 
 double tile_us(const TileCost &c, int64_t steps) { return c.fixed + c.step * (double)ceil_div(steps, c.groups); }
@@ -282,7 +283,9 @@ int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, hipStre
     if (g_force_merge == 9) best_us = 1e30;
     if (g_force_merge >= 0 && g_force_merge < 9) { best = g_force_merge; best_us = 0; }
 #endif
-    if (n < 2 || apart <= best_us) {
+    // (together, large products share the caches less: 2048 rows x 2048 x 4096
+    // and smaller gain 5 to 35%, 8192 x 4096 x 11008 loses 3%)
+    if (n < 2 || apart <= 1.06 * best_us) {
         for (int i = 0; i < n; ++i) {
             const hipError_t e = i == 0 && with_dx ? dense_dx_launch(p[i], plans[i].tile, st) : dense_dw_launch(p[i], plans[i].tile, st);
             if (e != hipSuccess) return MOE_ERR_LAUNCH;
