@@ -52,6 +52,12 @@ __device__ __forceinline__ void dn_load_lds(u32x4 rsrc, uint32_t dst, uint32_t o
                  : "memory", "m0");
 }
 
+// a constant as an argument
+template <int N>
+struct DnInt {
+    static constexpr int value = N;
+};
+
 // ---------------------------------------------------------------------------
 // Values and types
 // ---------------------------------------------------------------------------
@@ -170,11 +176,37 @@ __device__ __forceinline__ float dn_act1(int act, float v, float &d) {
             return v;
     }
 }
+// V values at once: f(constant activation) for a run-time one, so that one
+// activation's code runs straight through
+template <class F>
+__device__ __forceinline__ void dn_for_act(int act, F f) {
+    switch (act) {
+        case DN_ACT_SILU: f(DnInt<DN_ACT_SILU>()); break;
+        case DN_ACT_GELU: f(DnInt<DN_ACT_GELU>()); break;
+        case DN_ACT_GELU_TANH: f(DnInt<DN_ACT_GELU_TANH>()); break;
+        case DN_ACT_RELU: f(DnInt<DN_ACT_RELU>()); break;
+        default: break;
+    }
+}
 template <int V>
 __device__ __forceinline__ void dn_act(int act, float (&v)[V]) {
-    float d;
+    dn_for_act(act, [&](auto a) {
+        float d;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = dn_act1<false>(act, v[i], d);
+        for (int i = 0; i < V; ++i) v[i] = dn_act1<false>(decltype(a)::value, v[i], d);
+    });
+}
+// v *= act'(z)
+template <int V>
+__device__ __forceinline__ void dn_times_slope(int act, const float (&z)[V], float (&v)[V]) {
+    dn_for_act(act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float d;
+            dn_act1<true>(decltype(a)::value, z[i], d);
+            v[i] *= d;
+        }
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -404,10 +436,6 @@ __device__ __forceinline__ void dn_tile(const DenseParams &P, int b, int &tm, in
     tm = grp * G + in - tn * rows;
 }
 
-template <int N>
-struct DnInt {
-    static constexpr int value = N;
-};
 struct DnTrue {
     static constexpr bool value = true;
 };
@@ -910,17 +938,49 @@ __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense(Dense
 #endif
 }
 
+// Bias gradient: the row chunks' sums (no chunk: zero).  DN_SUM_COLS columns a
+// workgroup; each of its chunk lanes adds every THREADS / DN_SUM_COLS-th
+// chunk, then they are joined in order.
+constexpr int DN_SUM_COLS = 32;
+template <int THREADS>
+__device__ __forceinline__ void dn_colsum(const ColsumParams &P, int block, float *sums) {
+    constexpr int LANES = THREADS / DN_SUM_COLS, LD = DN_SUM_COLS + 1;
+    const int cl = threadIdx.x % DN_SUM_COLS, l = threadIdx.x / DN_SUM_COLS;
+    const int c = block * DN_SUM_COLS + cl;
+    float v = 0.f;
+    if (c < P.N) {
+#pragma unroll 8
+        for (int i = l; i < P.nchunks; i += LANES) v += P.part[(int64_t)i * P.N + c];
+    }
+    sums[l * LD + cl] = v;
+    __syncthreads();
+    if (l > 0 || c >= P.N) return;
+#pragma unroll
+    for (int i = 1; i < LANES; ++i) v += sums[i * LD + cl];
+    if (P.out_f32) {
+        float *o = (float *)P.out + c;
+        *o = P.accumulate ? *o + v : v;
+    } else {
+        uint16_t *o = (uint16_t *)P.out + c;
+        if (P.accumulate) v += dn_bf(*o);
+        *o = (uint16_t)(dn_pack(v, 0.f) & 0xFFFFu);
+    }
+}
+
 // A backward pass's last products, which do not depend on each other, in one
 // launch: the input gradient (A B) and the weight gradients (A^T B), those
-// with the longest tiles first.  Apart they would each end in a round of
-// tiles that leaves CUs idle, and wait for the launch before them.
+// with the longest tiles first, then the bias gradient's sums.  Apart they
+// would each end in a round of tiles that leaves CUs idle, and wait for the
+// launch before them.
 template <int BM, int BN, int WM, int WN, int KG, int D>
 __global__ __launch_bounds__(WM *WN *KG * 64, WM *WN *KG / 4) void k_dense_grads(DenseGradsParams A) {
 #ifdef __HIP_DEVICE_COMPILE__
     __shared__ __align__(1024) uint8_t smem[DN_LDS<BM, BN, KG, D>];
     int b = blockIdx.x, i = 0;
-    while (b >= A.tiles[i]) b -= A.tiles[i++];  // (the grid is the sum of the tiles)
-    if (i == A.dx_at)
+    while (i < A.n && b >= A.tiles[i]) b -= A.tiles[i++];
+    if (i == A.n)
+        dn_colsum<WM * WN * KG * 64>(A.sum, b, (float *)smem);
+    else if (i == A.dx_at)
         dense_body<BM, BN, WM, WN, KG, D, DN_NN, DN_EPI_LINEAR, DN_ACT_NONE>(A.p[i], b, 0, smem);
     else
         dense_body<BM, BN, WM, WN, KG, D, DN_TN, DN_EPI_LINEAR, DN_ACT_NONE>(A.p[i], b, 0, smem);

@@ -250,9 +250,9 @@ inline hipStream_t S(int64_t s) { return (hipStream_t)(intptr_t)s; }
 int launch_err(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 
 // A backward pass's last products (p[0] dx where with_dx, the rest weight
-// gradients), each with the plan of a launch of its own: one launch of all
-// where its estimate is lower.
-int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, hipStream_t st) {
+// gradients), each with the plan of a launch of its own, and the bias
+// gradient's sums (sum.out): one launch of all where its estimate is lower.
+int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, const ColsumParams &sum, hipStream_t st) {
     int order[DN_MAX_GRADS];
     double apart = 0.0;
     for (int i = 0; i < n; ++i) {  // longest tiles first
@@ -286,6 +286,7 @@ int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, hipStre
     // (together, large products share the caches less: 2048 rows x 2048 x 4096
     // and smaller gain 5 to 35%, 8192 x 4096 x 11008 loses 3%)
     if (n < 2 || apart <= 1.06 * best_us) {
+        if (sum.out && dense_colsum_launch(sum, st) != hipSuccess) return MOE_ERR_LAUNCH;
         for (int i = 0; i < n; ++i) {
             const hipError_t e = i == 0 && with_dx ? dense_dx_launch(p[i], plans[i].tile, st) : dense_dw_launch(p[i], plans[i].tile, st);
             if (e != hipSuccess) return MOE_ERR_LAUNCH;
@@ -296,6 +297,7 @@ int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, hipStre
     memset(&A, 0, sizeof(A));
     A.n = n;
     A.dx_at = -1;
+    A.sum = sum;
     const TileCost &c = TILES[best];
     for (int i = 0; i < n; ++i) {
         DenseParams &q = A.p[i];
@@ -418,7 +420,6 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
     const bool with_act = act != MOE_ACT_NONE;
     const uint16_t *dz = with_act ? (const uint16_t *)at(ws, L.dz) : (const uint16_t *)dy;
     int nchunks = 0;
-    bool summed = false;
     if (T != 0 && (with_act || dbias)) {
         DzParams D;
         memset(&D, 0, sizeof(D));
@@ -429,20 +430,12 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
         D.T = T;
         D.N = out;
         D.act = act;
-        // chunks of at least 16 rows, at most DN_DZ_CHUNKS of them
-        D.rows_per_chunk = max64(ceil_div(T, DN_DZ_CHUNKS), 16);
+        // chunks of at least 32 rows, at most DN_DZ_CHUNKS of them
+        D.rows_per_chunk = max64(ceil_div(T, DN_DZ_CHUNKS), 32);
         nchunks = D.nchunks = (int)ceil_div(T, D.rows_per_chunk);
-        D.counters = (uint32_t *)ws;
-        D.out = ceil_div(out, 256) <= WS_COUNTERS ? dbias : nullptr;
-        D.out_f32 = dw_dtype == MOE_DTYPE_F32;
-        D.accumulate = accumulate != 0;
-        summed = D.out != nullptr;
         if (dense_dz_launch(D, st) != hipSuccess) return MOE_ERR_LAUNCH;
     }
-    if (dbias && !summed) {
-        ColsumParams C{(const float *)at(ws, L.chunks), dbias, out, nchunks, dw_dtype == MOE_DTYPE_F32, accumulate != 0};
-        if (dense_colsum_launch(C, st) != hipSuccess) return MOE_ERR_LAUNCH;
-    }
+    const ColsumParams sum{(const float *)at(ws, L.chunks), dbias, out, nchunks, dw_dtype == MOE_DTYPE_F32, accumulate != 0};
     DenseParams P[2];
     Plan plans[2];
     int n = 0;
@@ -461,7 +454,7 @@ int moe_linear_backward(const void *dy, int32_t T, int32_t in, int32_t out, cons
                            L.bpart);
         plans[n++] = L.dw;
     }
-    return launch_grads(P, plans, n, with_dx, st);
+    return launch_grads(P, plans, n, with_dx, sum, st);
 }
 
 int64_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t hidden, int32_t ffn) {
@@ -594,7 +587,9 @@ int moe_gated_ffn_backward(const void *dy, const void *x, int32_t T, const moe_d
     grad(dgu, 2 * (int64_t)F, x, F, H, L.dw, dgate);
     grad(dgu + F, 2 * (int64_t)F, x, F, H, L.dw, dup);
     grad((const uint16_t *)dy, H, h, H, F, L.dd, ddown);
-    return launch_grads(P, plans, n, with_dx, st);
+    ColsumParams none;
+    memset(&none, 0, sizeof(none));
+    return launch_grads(P, plans, n, with_dx, none, st);
 }
 
 }  // extern "C"

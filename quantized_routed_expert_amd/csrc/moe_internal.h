@@ -315,15 +315,6 @@ struct DenseParams {
     int splits, steps_per_split;
 };
 
-// The products of a backward pass that run side by side, longest tiles first:
-// p[dx_at] is dx (A B; -1: none), the others weight gradients (A^T B);
-// tiles[i]: the tiles of p[i].
-constexpr int DN_MAX_GRADS = 4;
-struct DenseGradsParams {
-    DenseParams p[DN_MAX_GRADS];
-    int tiles[DN_MAX_GRADS], n, dx_at;
-};
-
 // Few rows (a decode window): C = A B^T by streaming B once, k split over
 // waves; A in bf16 or fp32.
 constexpr int DN_ROWS_MAX = 64;
@@ -345,15 +336,24 @@ struct DzParams {
     const uint16_t *dy, *z;  // [T][N]; z null: no activation
     uint16_t *dz;            // [T][N] or null
     float *part;             // [nchunks][N] or null
-    uint32_t *counters;      // one per 256 columns, DEC_CSTRIDE words apart (zero between calls)
-    void *out;               // [N] the sums, or null: by k_dense_colsum
     int64_t rows_per_chunk;
-    int T, N, nchunks, act, out_f32, accumulate;
+    int T, N, nchunks, act;
 };
+// ... and their sum: the bias gradient
 struct ColsumParams {
     const float *part;  // [nchunks][N]
     void *out;          // [N]
     int N, nchunks, out_f32, accumulate;
+};
+
+// The products of a backward pass that run side by side, longest tiles first:
+// p[dx_at] is dx (A B; -1: none), the others weight gradients (A^T B);
+// tiles[i]: the tiles of p[i].
+constexpr int DN_MAX_GRADS = 4;
+struct DenseGradsParams {
+    DenseParams p[DN_MAX_GRADS];
+    ColsumParams sum;  // out null: none
+    int tiles[DN_MAX_GRADS], n, dx_at;
 };
 
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

@@ -16,17 +16,6 @@ __global__ __launch_bounds__(256) void k_dense_split3(const float *x, uint16_t *
     }
 }
 
-__device__ __forceinline__ void dn_store_sum(void *out, int c, float v, int out_f32, int accumulate) {
-    if (out_f32) {
-        float *o = (float *)out + c;
-        *o = accumulate ? *o + v : v;
-    } else {
-        uint16_t *o = (uint16_t *)out + c;
-        if (accumulate) v += dn_bf(*o);
-        *o = (uint16_t)(dn_pack(v, 0.f) & 0xFFFFu);
-    }
-}
-
 // dz = dy act'(z) for 256 columns (32 threads of 8) and one chunk of rows (8
 // at a time), and the chunk's column sums (from the unrounded values: eight
 // row lanes in fp32, then joined in order).  Bound by its reads and writes.
@@ -38,23 +27,30 @@ __global__ __launch_bounds__(256) void k_dense_dz(DzParams P) {
     const int64_t r1 = min((int64_t)P.T, r0 + P.rows_per_chunk);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n < P.N) {
-#pragma unroll 4
-        for (int64_t t = r0 + rl; t < r1; t += 8) {
-            float v[8];
-            dn_load_bf<8>(P.dy + t * P.N + n, v);
-            if (P.z) {
-                float z[8];
-                dn_load_bf<8>(P.z + t * P.N + n, z);
+        constexpr int Q = 4;  // rows in flight per thread (loaded before the first is stored)
+        for (int64_t t0 = r0 + rl; t0 < r1; t0 += 8 * Q) {
+            u32x4 dy[Q], z[Q];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float d;
-                    dn_act1<true>(P.act, z[i], d);
-                    v[i] *= d;
-                }
+            for (int q = 0; q < Q; ++q) {
+                const int64_t t = min(t0 + 8 * q, r1 - 1);
+                dy[q] = *(const u32x4 *)(P.dy + t * P.N + n);
+                if (P.z) z[q] = *(const u32x4 *)(P.z + t * P.N + n);
             }
-            if (P.dz) dn_store_bf<8>(P.dz + t * P.N + n, v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += v[i];
+            for (int q = 0; q < Q; ++q) {
+                const int64_t t = t0 + 8 * q;
+                if (t >= r1) break;
+                float v[8];
+                dn_unpack<8>(dy[q], v);
+                if (P.z) {
+                    float zv[8];
+                    dn_unpack<8>(z[q], zv);
+                    dn_times_slope<8>(P.act, zv, v);
+                }
+                if (P.dz) dn_store_bf<8>(P.dz + t * P.N + n, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] += v[i];
+            }
         }
     }
     if (!P.part) return;
@@ -66,39 +62,13 @@ __global__ __launch_bounds__(256) void k_dense_dz(DzParams P) {
         float v = s_sum[0][tid];
 #pragma unroll
         for (int i = 1; i < 8; ++i) v += s_sum[i][tid];
-        if (P.out)
-            __hip_atomic_store(&P.part[(int64_t)blockIdx.y * P.N + c], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        else
-            P.part[(int64_t)blockIdx.y * P.N + c] = v;
+        P.part[(int64_t)blockIdx.y * P.N + c] = v;
     }
-    // the last workgroup of these columns adds the chunks, in order
-    __shared__ uint32_t s_last;
-    if (!P.out || !dn_last(P.counters + (int64_t)blockIdx.x * DEC_CSTRIDE, (uint32_t)P.nchunks, &s_last) || c >= P.N) return;
-    float v = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < P.nchunks; ++i)
-        v += __hip_atomic_load(&P.part[(int64_t)i * P.N + c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    dn_store_sum(P.out, c, v, P.out_f32, P.accumulate);
 }
 
-// bias gradient where k_dense_dz does not finish it (no rows, or more columns
-// than counters): the chunks' sums.  32 columns a workgroup; eight chunk lanes
-// add every eighth chunk, then are joined in order (nchunks 0: zero).
 __global__ __launch_bounds__(256) void k_dense_colsum(ColsumParams P) {
-    __shared__ float s_sum[8][33];
-    const int cl = threadIdx.x & 31, l = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + cl;
-    float v = 0.f;
-    if (c < P.N) {
-#pragma unroll 8
-        for (int i = l; i < P.nchunks; i += 8) v += P.part[(int64_t)i * P.N + c];
-    }
-    s_sum[l][cl] = v;
-    __syncthreads();
-    if (l > 0 || c >= P.N) return;
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v += s_sum[i][cl];
-    dn_store_sum(P.out, c, v, P.out_f32, P.accumulate);
+    __shared__ float s_sum[256 / DN_SUM_COLS][DN_SUM_COLS + 1];
+    dn_colsum<256>(P, blockIdx.x, &s_sum[0][0]);
 }
 
 hipError_t dense_split3_launch(const float *x, uint16_t *out, int64_t n, hipStream_t st) {
@@ -111,7 +81,7 @@ hipError_t dense_dz_launch(const DzParams &P, hipStream_t st) {
     return hipGetLastError();
 }
 hipError_t dense_colsum_launch(const ColsumParams &P, hipStream_t st) {
-    hipLaunchKernelGGL(k_dense_colsum, dim3((unsigned)((P.N + 31) / 32)), dim3(256), 0, st, P);
+    hipLaunchKernelGGL(k_dense_colsum, dim3((unsigned)((P.N + DN_SUM_COLS - 1) / DN_SUM_COLS)), dim3(256), 0, st, P);
     return hipGetLastError();
 }
 hipError_t dense_linear_launch(const DenseParams &P, int tile, hipStream_t st) {
