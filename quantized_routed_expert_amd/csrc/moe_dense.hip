@@ -121,9 +121,6 @@ double tiles_us(const double *us, const int64_t *n, int k) {
     return last;
 }
 
-#ifdef DN_FORCE
-int g_force_tile = -1, g_force_split = 1, g_force_rows = -1, g_force_merge = -1;
-#endif
 // C of M x N columns of the weight side (gated: 2F) over `steps` 64-k steps
 Plan make_plan(int64_t M, int64_t N, int64_t steps) {
     Plan best = {-1, 0, 0, 1, 1, 1e30};
@@ -132,9 +129,6 @@ Plan make_plan(int64_t M, int64_t N, int64_t steps) {
         const TileCost &c = TILES[t];
         const int64_t tm = ceil_div(M, c.bm), tn = ceil_div(N, c.bn), tiles = max64(tm * tn, 1);  // (M = 0: nothing is launched)
         for (int64_t s = 1; s <= 16; s *= 2) {
-#ifdef DN_FORCE
-            if (g_force_tile >= 0 && (t != g_force_tile || s != g_force_split)) continue;
-#endif
             if (s > 1 && (tiles * s * c.bm * c.bn > (int64_t)DN_SPLIT_TILES * 128 * 128 || tiles > WS_COUNTERS ||
                           steps < 2 * s * c.groups))
                 break;
@@ -164,9 +158,6 @@ double rows_us(int64_t T, int64_t K, int64_t rows, bool x_f32) {
 }
 bool few_rows(int64_t T, int64_t K, int64_t rows, bool x_f32, const Plan &tiles) {
     if (T > DN_ROWS_MAX) return false;
-#ifdef DN_FORCE
-    if (g_force_rows >= 0) return T <= g_force_rows;
-#endif
     return rows_us(T, K, rows, x_f32) < tiles.us + (x_f32 ? 2.7 : 0.0);  // (tiles: fp32 is split by a launch of its own)
 }
 
@@ -269,7 +260,9 @@ int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, const C
         int64_t tiles[DN_MAX_GRADS];
         for (int i = 0; i < n; ++i) {
             const DenseParams &q = p[order[i]];
-            us[i] = tile_us(c, q.steps);
+            // (tiles of 64 columns read most per product: with all CUs at work the
+            // caches hold them up; 777 x 1032 x 2048: 23 us, in 128 x 128 tiles 19.5)
+            us[i] = tile_us(c, q.steps) * (c.bn == 64 ? 1.25 : 1.0);
             tiles[i] = ceil_div(q.M, c.bm) * ceil_div(q.N, c.bn);
             out += out_us(q.M, q.N);
         }
@@ -279,10 +272,6 @@ int launch_grads(DenseParams *p, const Plan *plans, int n, bool with_dx, const C
             best = t;
         }
     }
-#ifdef DN_FORCE
-    if (g_force_merge == 9) best_us = 1e30;
-    if (g_force_merge >= 0 && g_force_merge < 9) { best = g_force_merge; best_us = 0; }
-#endif
     // (together, large products share the caches less: 2048 rows x 2048 x 4096
     // and smaller gain 5 to 35%, 8192 x 4096 x 11008 loses 3%)
     if (n < 2 || apart <= 1.06 * best_us) {
@@ -342,11 +331,6 @@ int x_segments(DenseParams &P, const void *x, bool x_f32, int64_t T, int64_t K, 
 }  // namespace
 
 extern "C" {
-#ifdef DN_FORCE
-void dn_force_rows(int r) { g_force_rows = r; }
-void dn_force_merge(int r) { g_force_merge = r; }
-void dn_force(int tile, int split) { g_force_tile = tile; g_force_split = split; }
-#endif
 
 int64_t moe_linear_workspace_bytes(int32_t T, int32_t in, int32_t out) {
     int rc = check_rows(T);
