@@ -13,6 +13,11 @@
 //
 // A bf16 activation is an operand as it is; an fp32 one enters as its three
 // exact bf16 terms (three MFMAs on one weight fragment).
+//
+// Measured (MI355X, kernel alone in a graph): 1 x 2048 x 2048 3.6 us, 16 rows
+// 5.3; 1 x 4096 x 22016 35 us (5.1 TB/s of weights); fp32 37 x 1000 x 520
+// 8.4 us, most of it splitting the activations.  Tiles take over where a
+// workgroup's activation reads outweigh its weights (moe_dense.hip).
 #include "moe_dense.h"
 
 namespace moe {

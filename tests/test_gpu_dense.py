@@ -215,6 +215,68 @@ def test_gated_backward_parts(want):
     gated_backward_case(40, 72, 136, moe.ACT_SILU, BF, True, want)
 
 
+# Sizes that take each tile shape, whole and split, in each form (odd tails in all of them).
+@pytest.mark.parametrize("T,K,N", [(257, 200, 5584), (130, 136, 5464), (17, 2400, 8), (257, 72, 5448), (2050, 136, 3640),
+                                   (130, 2016, 8), (70, 72, 136), (16, 136, 6000), (5, 520, 4200)])
+def test_every_tile_forward(T, K, N):
+    linear_case(T, K, N, moe.ACT_GELU_TANH, BF, F32, F32, True, True)
+    linear_case(T, K, N, moe.ACT_NONE, BF, BF, F32, False, False)
+    gated_case(T, K, N, moe.ACT_SILU, BF, BF, BF, True)
+
+
+@pytest.mark.parametrize("T,H,Fw", [(130, 200, 4168), (70, 72, 4192), (130, 72, 4104), (777, 72, 4136), (16, 72, 4200)])
+def test_every_tile_gated(T, H, Fw):
+    gated_case(T, H, Fw, moe.ACT_GELU, BF, F32, F32, False)
+
+
+@pytest.mark.parametrize("T,K,N", [(777, 2352, 200), (777, 584, 7512), (400, 2416, 8), (17, 8, 1800), (777, 2320, 72),
+                                   (17, 8, 2024), (2050, 3640, 72)])
+def test_every_tile_dx(T, K, N):
+    linear_backward_case(T, K, N, moe.ACT_NONE, BF, False, ("dx",))
+
+
+@pytest.mark.parametrize("T,K,N", [(257, 264, 6608), (17, 136, 5584), (2050, 8, 8), (17, 264, 6608), (17, 1032, 7208), (2050, 96, 8)])
+@pytest.mark.parametrize("wd,accumulate", [(BF, False), (F32, True)])
+def test_every_tile_dw(T, K, N, wd, accumulate):
+    linear_backward_case(T, K, N, moe.ACT_NONE, wd, accumulate, ("dw",))
+
+
+@pytest.mark.parametrize("T,H,Fw", [(257, 200, 5584), (130, 72, 5464), (17, 1808, 8), (257, 72, 5448), (2050, 72, 3640)])
+def test_every_tile_gated_backward(T, H, Fw):
+    gated_backward_case(T, H, Fw, moe.ACT_GELU_TANH, BF, False, ("ddown",))
+    gated_backward_case(T, H, Fw, moe.ACT_SILU, F32, True)
+
+
+def test_gradients_together_in_large_tiles():
+    linear_backward_case(2100, 2104, 2104, moe.ACT_SILU, F32, True)
+
+
+def test_offsets_past_32_bits():
+    """Rows whose byte offsets pass 2^32 in x, z and y (bf16, 4.4 GB each): the last rows against the definition."""
+    T, K, N = 1 << 20, 2104, 2104
+    g = gen(9)
+    w = rnd(g, N, K, std=ref.weight_std(K))
+    x = torch.zeros(T, K, dtype=BF, device=DEV)
+    x[-300:] = rnd(g, 300, K)
+    ws = moe.linear_workspace(T, K, N)
+    y, z = torch.full((T, N), 5.0, dtype=BF, device=DEV), torch.full((T, N), 5.0, dtype=BF, device=DEV)
+    moe.linear(x, w, ws, act=moe.ACT_RELU, z=z, y=y)
+    torch.cuda.synchronize()
+    want = ref.linear(x[-300:], w, None, moe.ACT_RELU, None, BF, True)
+    ref.check("y", y[-300:], want["y"])
+    ref.check("z", z[-300:], want["z"])
+    assert (y[:-300] == 0).all() and (z[:-300] == 0).all()
+    dx, dw = torch.empty_like(x), torch.empty(N, K, device=DEV)
+    dy = torch.zeros(T, N, dtype=BF, device=DEV)
+    dy[-300:] = rnd(g, 300, N, std=0.1)
+    moe.linear_backward(dy, x, w, ws, dx=dx, dw=dw)
+    torch.cuda.synchronize()
+    r = ref.linear_backward(dy[-300:], x[-300:], w, None, moe.ACT_NONE, F32)
+    ref.check("dx", dx[-300:], r["dx"])
+    ref.check("dw", dw, (r["dw"][0], r["dw"][1]))
+    assert (dx[:-300] == 0).all()
+
+
 def test_no_rows():
     """T = 0: outputs of no rows; weight gradients zero, or as they were when accumulating."""
     K, N = 72, 136
