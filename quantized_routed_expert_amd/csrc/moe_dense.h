@@ -811,7 +811,7 @@ __device__ __forceinline__ void dense_body(const DenseParams &P, int tile, int s
             constexpr int V = decltype(width)::value, IN = decltype(reads)::value, SUB = 8 / V;
             const DenseEpi &e = P.e;
             // row blocks whose input is in flight ahead of their use
-            constexpr int AHEAD = IN == 0 ? 1 : IN == 2 && V == 8 ? 2 : 4;  // (what the registers hold)
+            constexpr int AHEAD = IN == 0 ? 1 : IN == 2 && V == 8 ? 2 : 3;  // (what the registers hold)
             constexpr int PRE = MS < AHEAD ? MS : AHEAD;
             constexpr int LD = EPI == DN_EPI_DGATED ? 2 : 1;
             u32x4 in[PRE][UJ][SUB][2];
