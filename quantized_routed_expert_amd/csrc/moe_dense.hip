@@ -141,16 +141,15 @@ Plan make_plan(int64_t M, int64_t N, int64_t steps) {
     return best;
 }
 
-// The few-row kernel against tiles: a workgroup takes 16 weight rows (8 up to
-// 16 activation rows while that is at most two per CU) and reads its
-// activation rows from L2, together 35 KB a microsecond; all weights at most
-// 5.1 TB/s.  (T, K, N = 16, 2048, 2048: 5.3 us and 8.4 with tiles; 16, 2048,
-// 11264: 13.8 and 11.2; 64, 2048, 2048: 11.3 and 8.8; 37, 1000, 520: 4.2 and
-// 6.4.)
+// The few-row kernel against tiles: a workgroup reads its weight rows and its
+// activation rows (from L2), together 35 KB a microsecond; all weights at most
+// 5.1 TB/s.  (T, K, N = 16, 2048, 2048: 5.2 us and 8.4 with tiles; 16, 2048,
+// 11264: 13.8 and 11.2; 64, 2048, 2048: 7.9 and 8.8; 37, 1000, 520: 3.3 and
+// 6.4, with fp32 activations 4.5 and 16.9.)
 double rows_us(int64_t T, int64_t K, int64_t rows, bool x_f32) {
-    const bool halves = T <= 16 && ceil_div(rows, 16) <= CUS;
-    const int64_t wr = halves ? 8 : 16, wgs = ceil_div(rows, wr);
-    const int64_t xr = T == 1 ? 1 : ceil_div(T, wr) * wr;  // (one row: every lane's load is the same)
+    const DenseRowsShape s = dense_rows_shape(T, rows);
+    const int64_t wr = s.halves ? 8 : 16, wgs = s.wgs * s.blocks;
+    const int64_t xr = T == 1 ? 1 : s.mt * wr;  // (one row: every lane's load is the same)
     const double bytes = (double)K * (double)(2 * wr + (x_f32 ? 5 : 2) * xr);
     const double rounds = wgs > CUS ? (double)wgs / CUS : 1.0;
     const double us = rounds * bytes / 35e3, hbm = (double)K * (double)rows * 2.0 / 5.1e6;

@@ -325,6 +325,29 @@ struct DenseRowsParams {
     int M, N, K, a_f32;
 };
 
+// How the few-row kernel shares M activation rows and `rows` weight rows: 16
+// weight rows a workgroup (8, with operand halves at two parts of K, up to 16
+// activation rows while that is at most two workgroups per CU) and mt blocks of
+// 16 (8) activation rows, the least that keeps one workgroup per CU.
+struct DenseRowsShape {
+    bool halves;
+    int mt, blocks;  // blocks: workgroups along the activation rows
+    int64_t wgs;     // ... along the weight rows
+};
+inline DenseRowsShape dense_rows_shape(int64_t M, int64_t rows) {
+    constexpr int64_t CUS = 256;
+    DenseRowsShape s;
+    s.wgs = (rows + 15) / 16;
+    s.halves = M <= 16 && s.wgs <= CUS;
+    const int64_t block = s.halves ? 8 : 16;
+    s.wgs = (rows + block - 1) / block;
+    for (s.mt = 1;; s.mt *= 2) {
+        s.blocks = (int)((M + block * s.mt - 1) / (block * s.mt));
+        if (s.blocks <= 1 || s.wgs * s.blocks <= CUS || s.mt == 4) break;
+    }
+    return s;
+}
+
 // product forms: C = A B^T (rows of both run along k), C = A B (B's rows run
 // along n), C = A^T B (rows of A run along m, of B along n)
 enum DenseForm { DN_NT = 0, DN_NN = 1, DN_TN = 2 };

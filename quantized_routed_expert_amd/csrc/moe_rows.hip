@@ -15,8 +15,9 @@
 // exact bf16 terms (three MFMAs on one weight fragment).
 //
 // Measured (MI355X, kernel alone in a graph): 1 x 2048 x 2048 3.6 us, 16 rows
-// 5.3; 1 x 4096 x 22016 35 us (5.1 TB/s of weights); fp32 37 x 1000 x 520
-// 8.4 us, most of it splitting the activations.  Tiles take over where a
+// 5.2, 64 rows 7.9; 1 x 4096 x 22016 35 us (5.1 TB/s of weights); fp32 37 x
+// 1000 x 520 4.5 us (8.4 with all rows in one workgroup, which then splits
+// them all).  Tiles take over where a
 // workgroup's activation reads outweigh its weights (moe_dense.hip).
 #include "moe_dense.h"
 
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lg = lane >> 4;
     const int half = HALVES == 2 ? li >> 3 : 0, r = HALVES == 2 ? li & 7 : li;
-    const int n0 = blockIdx.x * RN;
+    const int n0 = blockIdx.x * RN, m0 = blockIdx.y * (MT * 16 / HALVES);
     // rows past the end read a valid row and are never stored
     const int n = min(n0 + (GATED ? r % RN : r), P.N - 1);
     const uint16_t *wr = (GATED && r >= RN ? P.b2 : P.b) + (int64_t)n * P.K;
@@ -70,7 +71,7 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
                 s.w[i] = *(const u32x4 *)(wr + k);
 #pragma unroll
                 for (int q = 0; q < MT; ++q) {
-                    const int64_t at = (int64_t)min(16 / HALVES * q + r, P.M - 1) * P.K + k;
+                    const int64_t at = (int64_t)min(m0 + 16 / HALVES * q + r, P.M - 1) * P.K + k;
                     if constexpr (XF32) {
                         s.x[i][q][0] = *(const u32x4 *)((const float *)P.a + at);
                         s.x[i][q][1] = *(const u32x4 *)((const float *)P.a + at + 4);
@@ -128,13 +129,13 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
     }
     __syncthreads();
     constexpr int Q = RN / 4;  // four columns per thread
-    const int m = tid / Q, c = tid % Q * 4;
-    if (m >= P.M || n0 + c >= P.N) return;
+    const int ml = tid / Q, m = m0 + ml, c = tid % Q * 4;
+    if (ml >= MT * 16 / HALVES || m >= P.M || n0 + c >= P.N) return;
     float v[4], u[4];
     auto sum = [&](float(&o)[4], int col) {
-        float4v q = *(const float4v *)&s_part[0][m][col];
+        float4v q = *(const float4v *)&s_part[0][ml][col];
 #pragma unroll
-        for (int p = 1; p < PARTS; ++p) q += *(const float4v *)&s_part[p][m][col];
+        for (int p = 1; p < PARTS; ++p) q += *(const float4v *)&s_part[p][ml][col];
         o[0] = q.x;
         o[1] = q.y;
         o[2] = q.z;
@@ -151,34 +152,24 @@ __global__ __launch_bounds__(RW_WAVES * 64) void k_dense_rows(DenseRowsParams P)
 
 template <int EPI>
 static hipError_t rows_t(const DenseRowsParams &P, hipStream_t st) {
-    const int cols = EPI == DN_EPI_GATED ? 8 : 16;  // of a workgroup of 16 weight rows
-    const int64_t wgs = ((int64_t)P.N + cols - 1) / cols;
-    // 8 weight rows a workgroup while that leaves at most two per CU
-    const bool halves = P.M <= 16 && wgs <= 256;
-    const dim3 grid((unsigned)(halves ? ((int64_t)P.N + cols / 2 - 1) / (cols / 2) : wgs)), block(RW_WAVES * 64);
-#define RW_LAUNCH(XF32, HALVES, MT) hipLaunchKernelGGL((k_dense_rows<EPI, XF32, HALVES, MT>), grid, block, 0, st, P)
-    if (P.a_f32) {
-        if (halves && P.M <= 8)
-            RW_LAUNCH(1, 2, 1);
-        else if (halves)
-            RW_LAUNCH(1, 2, 2);
-        else if (P.M <= 16)
-            RW_LAUNCH(1, 1, 1);
-        else if (P.M <= 32)
-            RW_LAUNCH(1, 1, 2);
-        else
-            RW_LAUNCH(1, 1, 4);
+    const int64_t rows = EPI == DN_EPI_GATED ? 2 * (int64_t)P.N : P.N;
+    const DenseRowsShape S = dense_rows_shape(P.M, rows);
+    const dim3 grid((unsigned)S.wgs, (unsigned)S.blocks), block(RW_WAVES * 64);
+#define RW_LAUNCH(HALVES, MT)                                                                        \
+    if (P.a_f32)                                                                                     \
+        hipLaunchKernelGGL((k_dense_rows<EPI, 1, HALVES, MT>), grid, block, 0, st, P);                 \
+    else                                                                                             \
+        hipLaunchKernelGGL((k_dense_rows<EPI, 0, HALVES, MT>), grid, block, 0, st, P)
+    if (S.halves && S.mt == 1) {
+        RW_LAUNCH(2, 1);
+    } else if (S.halves) {
+        RW_LAUNCH(2, 2);
+    } else if (S.mt == 1) {
+        RW_LAUNCH(1, 1);
+    } else if (S.mt == 2) {
+        RW_LAUNCH(1, 2);
     } else {
-        if (halves && P.M <= 8)
-            RW_LAUNCH(0, 2, 1);
-        else if (halves)
-            RW_LAUNCH(0, 2, 2);
-        else if (P.M <= 16)
-            RW_LAUNCH(0, 1, 1);
-        else if (P.M <= 32)
-            RW_LAUNCH(0, 1, 2);
-        else
-            RW_LAUNCH(0, 1, 4);
+        RW_LAUNCH(1, 4);
     }
 #undef RW_LAUNCH
     return hipGetLastError();

@@ -291,16 +291,16 @@ def layer_forward_noalloc(x: torch.Tensor, logits: torch.Tensor, k: int, routed:
 _CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
-def _dense(name: str, t, shape: tuple, dtypes: tuple, dev: torch.device):
-    """Checks an operand of a dense operator (not None); returns its address."""
-    if t.shape == shape and t.dtype in dtypes and t.device == dev and t.is_contiguous():
+def _dense(name: str, t, shape: tuple, dtypes: tuple, dev: int):
+    """Checks an operand of a dense operator (not None) on device index dev (-1: the host); returns its address."""
+    if t.shape == shape and t.dtype in dtypes and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the other operands on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, other operands are on {f'cuda:{dev}' if dev >= 0 else 'the host'}")
     raise ValueError(f"{name} must be contiguous")
 
 
@@ -317,29 +317,30 @@ def _code(t) -> int:
 _ANY, _BF16 = (torch.float32, torch.bfloat16), (torch.bfloat16,)
 
 
-def _dense_device(x: torch.Tensor, ws: torch.Tensor) -> torch.device:
-    """The operands' device: a GPU, the current one (launches go there)."""
-    dev = x.device
-    if dev.type != "cuda":
+def _dense_device(x: torch.Tensor, ws: torch.Tensor) -> int:
+    """The operands' device index: a GPU, the current one (launches go there)."""
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError("dense operators take device tensors")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"operands on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {dev}")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"operands on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    if ws.get_device() != dev or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on cuda:{dev}")
     return dev
 
 
-def _dense_stream(stream, dev: torch.device) -> int:
+def _dense_stream(stream, dev: int) -> int:
     # (the current stream's handle without a Stream object: 0.1 us a call instead of 2.7)
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _dense_new(shape: tuple, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+def _dense_new(shape: tuple, dtype: torch.dtype, dev: int, stream) -> torch.Tensor:
     """A new output, allocated for the stream that writes it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-    with torch.cuda.stream(s):
+    if isinstance(stream, int):  # (0: the null stream)
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
@@ -408,12 +409,18 @@ def dense_ffn(gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, act: int
     """Describe a dense gated feed-forward block: gate, up [ffn, hidden] and
     down [hidden, ffn], bf16 device tensors (kept alive by the result)."""
     F, H = gate.shape
-    pg = _dense("gate", gate, (F, H), _BF16, gate.device)
-    pu = _dense("up", up, (F, H), _BF16, gate.device)
-    pd = _dense("down", down, (H, F), _BF16, gate.device)
+    pg = _dense("gate", gate, (F, H), _BF16, gate.get_device())
+    pu = _dense("up", up, (F, H), _BF16, gate.get_device())
+    pd = _dense("down", down, (H, F), _BF16, gate.get_device())
     d = DenseFFN(pg, pu, pd, H, F, act)
     d.tensors = (gate, up, down)
+    d.device = gate.get_device()
     return d
+
+
+def _ffn_device(ffn: DenseFFN, dev: int) -> None:
+    if getattr(ffn, "device", dev) != dev:  # (a description without tensors: its addresses are the caller's word)
+        raise ValueError(f"the block's weights are on device {ffn.device}, the other operands on cuda:{dev}")
 
 
 def gated_ffn_workspace_bytes(T: int, hidden: int, ffn: int) -> int:
@@ -434,6 +441,7 @@ def gated_ffn(x: torch.Tensor, ffn: DenseFFN, ws: torch.Tensor, residual=None, g
     the residual).  gu: bf16 [T, 2*ffn], receives gate and up for
     gated_ffn_backward."""
     dev = _dense_device(x, ws)
+    _ffn_device(ffn, dev)
     T = x.shape[0]
     H, F = ffn.hidden, ffn.ffn
     if y is None:
@@ -457,6 +465,7 @@ def gated_ffn_backward(dy: torch.Tensor, x, gu: torch.Tensor, ffn: DenseFFN, ws:
     with accumulate, the weight gradients are added to.  dy, x [T, hidden]
     bf16 (x is needed for dgate and dup); gu as gated_ffn wrote it."""
     dev = _dense_device(dy, ws)
+    _ffn_device(ffn, dev)
     T = dy.shape[0]
     H, F = ffn.hidden, ffn.ffn
     out = (T, H)

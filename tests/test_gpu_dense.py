@@ -383,6 +383,32 @@ def test_other_stream():
     ref.check("linear", b, ref.linear(x, gate, None, moe.ACT_NONE, None, BF)["y"])
 
 
+def test_null_stream_by_number():
+    g = gen(8)
+    x, w = rnd(g, 20, 136), rnd(g, 72, 136)
+    ws = moe.linear_workspace(20, 136, 72)
+    torch.cuda.synchronize()
+    y = moe.linear(x, w, ws, stream=0)
+    torch.cuda.synchronize()
+    ref.check("y", y, ref.linear(x, w, None, moe.ACT_NONE, None, BF)["y"])
+
+
+def test_block_on_another_device_refused():
+    g = gen(2)
+    w = rnd(g, 72, 64).cpu()
+    x = rnd(g, 4, 64)
+    with pytest.raises(ValueError):
+        moe.gated_ffn(x, moe.dense_ffn(w, w, w.T.contiguous()), moe.gated_ffn_workspace(4, 64, 72))
+
+
+@pytest.mark.parametrize("T", [9, 16, 17, 31, 33, 48, 49, 64])
+@pytest.mark.parametrize("N", [40, 2048, 5000])
+def test_few_rows(T, N):
+    """Every share of a window's rows among workgroups."""
+    linear_case(T, 264, N, moe.ACT_SILU, BF, BF, F32, True, True)
+    linear_case(T, 136, N, moe.ACT_NONE, F32, F32, None, False, False)
+
+
 def test_binding_refusals():
     g = gen(1)
     x, w, ws = rnd(g, 4, 64), rnd(g, 72, 64), moe.linear_workspace(4, 64, 72)
