@@ -145,7 +145,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t steps) {
 // activation rows (from L2), together 35 KB a microsecond; all weights at most
 // 5.1 TB/s.  (T, K, N = 16, 2048, 2048: 5.2 us and 8.4 with tiles; 16, 2048,
 // 11264: 13.8 and 11.2; 64, 2048, 2048: 7.9 and 8.8; 37, 1000, 520: 3.3 and
-// 6.4, with fp32 activations 4.5 and 16.9.)
+// 6.4, with fp32 activations 4.5 and 16.9; 256, 512, 512: 3.7 and 5.7.)
 double rows_us(int64_t T, int64_t K, int64_t rows, bool x_f32) {
     const DenseRowsShape s = dense_rows_shape(T, rows);
     const int64_t wr = s.halves ? 8 : 16, wgs = s.wgs * s.blocks;

@@ -317,7 +317,7 @@ struct DenseParams {
 
 // Few rows (a decode window): C = A B^T by streaming B once, k split over
 // waves; A in bf16 or fp32.
-constexpr int DN_ROWS_MAX = 64;
+constexpr int DN_ROWS_MAX = 256;
 struct DenseRowsParams {
     const void *a;             // [M][K]
     const uint16_t *b, *b2;    // [N][K] (b2: up)

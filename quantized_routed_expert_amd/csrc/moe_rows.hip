@@ -1,4 +1,4 @@
-// moe_rows.hip -- C = A B^T for few rows (M <= 64): the weights
+// moe_rows.hip -- C = A B^T for few rows (M <= 256): the weights
 // are read once, straight into the registers that the MFMA takes, and nothing
 // else costs: bound by the weights' bytes and, below some 10 MB, by the launch
 // and one round trip to memory.

@@ -401,7 +401,7 @@ def test_block_on_another_device_refused():
         moe.gated_ffn(x, moe.dense_ffn(w, w, w.T.contiguous()), moe.gated_ffn_workspace(4, 64, 72))
 
 
-@pytest.mark.parametrize("T", [9, 16, 17, 31, 33, 48, 49, 64])
+@pytest.mark.parametrize("T", [9, 16, 17, 31, 33, 48, 49, 64, 100, 200, 255, 256, 257])
 @pytest.mark.parametrize("N", [40, 2048, 5000])
 def test_few_rows(T, N):
     """Every share of a window's rows among workgroups."""
